@@ -397,6 +397,174 @@ int mamba2_ssd_state_update(float *state, const void *x, const void *dt, const f
                             const ms_ssd_update_dims *dims, int *dev_status, ms_stream_t stream);
 
 /*
+ * Linear attention with one decay per head. The SSD layer above decays its
+ * state by a step the input chooses; here the decay is a constant of the head,
+ * and queries, keys and values take the places of C, B and x. For sequence b
+ * and head h, with lam = exp(log_decay[h]), a the scale, and kv head
+ * g = h / (nheads / kv_heads) whose k and v the head reads:
+ *     S_t = lam S_{t-1} + k[b,t,g] v[b,t,g]^T        S is [dk, dv]
+ *     o[b,t,h] = a q[b,t,h] S_t
+ * log_decay [nheads] fp32 should be at most 0 (-inf: only the token itself is
+ * seen); it is not checked, and it is a constant: no gradient is formed.
+ * Layouts (element strides, the last dimension dense):
+ *   q [batch, seqlen, nheads, dk], k [batch, seqlen, kv_heads, dk],
+ *   v [batch, seqlen, kv_heads, dv], o [batch, seqlen, nheads, dv];
+ *   states [batch, nheads, dk, dv] fp32, dense.
+ * Packed sequences: with seq_start (device int32 [batch + 1], not decreasing)
+ * the arrays have no batch dimension: sequence i is rows seq_start[i] ..
+ * seq_start[i+1] - 1 of `total` rows; seqlen and the *_sb strides are not
+ * read. Lengths may be 0, and rows of no sequence are neither read nor
+ * written. A sequence whose rows are not within [0, total] in order is left
+ * out and MS_ERR_SHAPE is ORed into dev_status.
+ * dk and dv are 1..128, all arrays of one type, bf16 or fp32. bf16 rows that
+ * start on 16-byte boundaries (every pointer and stride) with dk and dv
+ * multiples of 8 run on the tcgen05 tensor cores in chunks of 128 tokens:
+ * the products' operands are bf16, so the scores (and, read by a query, the
+ * state) are rounded once to bf16; the running state itself stays fp32 and
+ * takes its updates at full precision. There, finite inputs are assumed: a
+ * non-finite value also spoils the other tokens of its chunk (never another
+ * sequence). Everything else runs a plain recurrence in fp32.
+ */
+typedef struct {
+    int64_t batch, seqlen, total, nheads, kv_heads, dk, dv;
+    int64_t q_sb, q_sl, q_sh;
+    int64_t k_sb, k_sl, k_sh;
+    int64_t v_sb, v_sl, v_sh;
+    int64_t o_sb, o_sl, o_sh;
+    int32_t dtype; /* q, k, v, o and their gradients */
+} ms_linattn_dims;
+
+/*
+ * Forward over whole sequences.
+ *   initial_state  optional (NULL = zero); final_state optional, and may be
+ *                  the same array (a sequence of length 0 passes it on).
+ *   workspace      device memory of mamba_linattn_workspace_size() bytes,
+ *                  16-byte aligned (NULL when that is 0): the states between
+ *                  the segments that a long sequence with few heads is cut
+ *                  into. Two calls in flight at once need two workspaces.
+ *                  `packed` is nonzero for a call with seq_start.
+ * Returns MS_OK or an MS_ERR_* code (MS_ERR_SHAPE for dk or dv outside
+ * [1, 128] or kv_heads not dividing nheads). dev_status receives
+ * MS_ERR_TIMEOUT if a bounded wait inside a kernel ran out (the results are
+ * then undefined).
+ */
+size_t mamba_linattn_workspace_size(const ms_linattn_dims *dims, int packed);
+int mamba_linattn_fwd(const void *q, const void *k, const void *v, const float *log_decay, float scale,
+                      const int32_t *seq_start, const float *initial_state, void *o, float *final_state,
+                      const ms_linattn_dims *dims, void *workspace, size_t workspace_bytes, int *dev_status,
+                      ms_stream_t stream);
+
+/*
+ * Gradients for a loss with dL/do = dout and dL/dfinal_state = dfinal (NULL =
+ * 0). dout has o's layout. With R the gradient of the state, R after the last
+ * token being dfinal, and R_t = a q_t dout_t^T + lam R_{t+1} (dfinal itself
+ * enters undecayed):
+ *     dq_t = a S_t dout_t      dk_t = R_t v_t      dv_t = R_t^T k_t
+ *     dinitial_state = lam R_0
+ * dk and dv of a shared kv head are sums over its heads, in a fixed order.
+ * dq, dk, dv have the layouts and strides of q, k, v; dinitial_state (fp32,
+ * dense; NULL = not wanted) must not be dfinal (MS_ERR_SHAPE). Each result is
+ * rounded once to its type. workspace: as for the forward, of
+ * mamba_linattn_bwd_workspace_size() bytes.
+ */
+size_t mamba_linattn_bwd_workspace_size(const ms_linattn_dims *dims, int packed);
+int mamba_linattn_bwd(const void *q, const void *k, const void *v, const float *log_decay, float scale,
+                      const int32_t *seq_start, const float *initial_state, const void *dout, const float *dfinal,
+                      void *dq, void *dk, void *dv, float *dinitial_state, const ms_linattn_dims *dims,
+                      void *workspace, size_t workspace_bytes, int *dev_status, ms_stream_t stream);
+
+/*
+ * One token (decode): S = lam S + k v^T in place, o = a q S with the new S.
+ * q, o [batch, nheads, .], k, v [batch, kv_heads, .] (element strides, last
+ * dimension dense); each head's [dk, dv] block of the state is dense. dk and
+ * dv are at least 1, dv at most 256.
+ */
+typedef struct {
+    int64_t batch, nheads, kv_heads, dk, dv;
+    int64_t q_sb, q_sh;
+    int64_t k_sb, k_sh;
+    int64_t v_sb, v_sh;
+    int64_t o_sb, o_sh;
+    int64_t state_sb, state_sh;
+    int32_t dtype; /* q, k, v, o */
+} ms_linattn_update_dims;
+
+int mamba_linattn_state_update(float *state, const void *q, const void *k, const void *v, const float *log_decay,
+                               float scale, void *o, const ms_linattn_update_dims *dims, int *dev_status,
+                               ms_stream_t stream);
+
+/*
+ * Gated norm behind a layer: `groups` root-mean-square norms over each row's
+ * width / groups columns, and the gate of the block. With n(a) = a /
+ * sqrt(mean(a^2) + eps) over a group:
+ *     y = n(x) w silu(z)          (gate_first zero)
+ *     y = n(x silu(z)) w          (gate_first nonzero, as the Mamba-2 block)
+ * x, z, y [rows, width] in one type with their own row strides; weight [width]
+ * fp32 (NULL = 1); z NULL = no gate. Statistics are fp32. A group is at most
+ * 16384 columns wide (MS_ERR_SHAPE).
+ */
+typedef struct {
+    int64_t rows, width, groups;
+    int64_t x_sr, z_sr, y_sr;
+    float eps;
+    int32_t dtype;
+    int32_t gate_first;
+} ms_gated_norm_dims;
+
+int mamba_gated_norm_fwd(const void *x, const void *z, const float *weight, void *y, const ms_gated_norm_dims *dims,
+                         int *dev_status, ms_stream_t stream);
+
+/*
+ * Its gradients for dL/dy = dy (strides y_sr). dx, dz [rows, width] dense in
+ * dims->dtype (dz NULL exactly where z is NULL); dweight [width] fp32 (NULL =
+ * not wanted), a sum over the rows in a fixed order through the workspace
+ * (mamba_gated_norm_bwd_workspace_size() bytes, 16-byte aligned; two calls in
+ * flight at once need two).
+ */
+size_t mamba_gated_norm_bwd_workspace_size(const ms_gated_norm_dims *dims);
+int mamba_gated_norm_bwd(const void *x, const void *z, const float *weight, const void *dy, void *dx, void *dz,
+                         float *dweight, const ms_gated_norm_dims *dims, void *workspace, size_t workspace_bytes,
+                         int *dev_status, ms_stream_t stream);
+
+/*
+ * Residual add and norm in front of the next layer: with s = res_scale and c
+ * the optional scale per channel,
+ *     residual_out = residual + s c x       y = n(residual_out) w
+ * x, y [rows, width] in dtype; residual (NULL = 0), residual_out (NULL = not
+ * wanted; may be residual itself) in res_dtype; weight, channel_scale [width]
+ * fp32 (NULL = 1). y is formed from the sum before its rounding to res_dtype.
+ * width is at most 16384.
+ */
+typedef struct {
+    int64_t rows, width;
+    int64_t x_sr, res_sr, y_sr, resout_sr;
+    float eps, res_scale;
+    int32_t dtype, res_dtype;
+} ms_residual_norm_dims;
+
+int mamba_residual_norm_fwd(const void *x, const void *residual, const float *weight, const float *channel_scale,
+                            void *y, void *residual_out, const ms_residual_norm_dims *dims, int *dev_status,
+                            ms_stream_t stream);
+
+/*
+ * Its gradients. residual_out is the forward's sum (strides resout_sr), dy the
+ * gradient of y (strides y_sr), dresidual_out the one that reaches the sum
+ * from the residual stream (res_dtype, strides res_sr; NULL = 0); x (strides
+ * x_sr) is read only with channel_scale and dchannel_scale. With r =
+ * residual_out and inv = 1 / sqrt(mean(r^2) + eps):
+ *     dresidual = dresidual_out + inv (dy w - r inv mean(dy w r inv))
+ *     dx = s c dresidual      dweight = sum dy r inv      dchannel_scale = sum s x dresidual
+ * dresidual [rows, width] in res_dtype and dx in dtype, dense; either may be
+ * NULL. dweight, dchannel_scale fp32 (NULL = not wanted), summed over the rows
+ * in a fixed order through the workspace, as above.
+ */
+size_t mamba_residual_norm_bwd_workspace_size(const ms_residual_norm_dims *dims);
+int mamba_residual_norm_bwd(const void *residual_out, const float *weight, const void *dy, const void *dresidual_out,
+                            const void *x, const float *channel_scale, void *dx, void *dresidual, float *dweight,
+                            float *dchannel_scale, const ms_residual_norm_dims *dims, void *workspace,
+                            size_t workspace_bytes, int *dev_status, ms_stream_t stream);
+
+/*
  * Sizes and strides of one decode step.
  *   x, delta, z, y : [batch, dim]     element (b,d) at b*x_sb + d
  *   B, C           : [batch, dstate]  element (b,n) at b*x_sb + n

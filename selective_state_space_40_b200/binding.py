@@ -61,6 +61,29 @@ class SsdUpdateDims(ctypes.Structure):
         "y_sb", "y_sh", "state_sb", "state_sh")] + [("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
+class LinattnDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "batch", "seqlen", "total", "nheads", "kv_heads", "dk", "dv", "q_sb", "q_sl", "q_sh", "k_sb", "k_sl", "k_sh",
+        "v_sb", "v_sl", "v_sh", "o_sb", "o_sl", "o_sh")] + [("dtype", ctypes.c_int32)]
+
+
+class LinattnUpdateDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "batch", "nheads", "kv_heads", "dk", "dv", "q_sb", "q_sh", "k_sb", "k_sh", "v_sb", "v_sh", "o_sb", "o_sh",
+        "state_sb", "state_sh")] + [("dtype", ctypes.c_int32)]
+
+
+class GatedNormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "width", "groups", "x_sr", "z_sr", "y_sr")] + [
+        ("eps", ctypes.c_float), ("dtype", ctypes.c_int32), ("gate_first", ctypes.c_int32)]
+
+
+class ResidualNormDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "width", "x_sr", "res_sr", "y_sr", "resout_sr")] + [
+        ("eps", ctypes.c_float), ("res_scale", ctypes.c_float), ("dtype", ctypes.c_int32),
+        ("res_dtype", ctypes.c_int32)]
+
+
 class MambaScanError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__(f"{what}: status {code} ({mamba_status_string(code)})")
@@ -141,6 +164,21 @@ def _load(path: str) -> ctypes.CDLL:
         lib.mamba_state_update.argtypes = [_vp] * 9 + [ctypes.c_int, _vp, ctypes.POINTER(UpdateDims),
                                                        _vp, _vp]
         lib.mamba_state_update.restype = ctypes.c_int
+        la, cint, size = ctypes.POINTER(LinattnDims), ctypes.c_int, ctypes.c_size_t
+        for fn, args, res in (
+                ("mamba_linattn_workspace_size", [la, cint], size),
+                ("mamba_linattn_bwd_workspace_size", [la, cint], size),
+                ("mamba_linattn_fwd", [_vp] * 4 + [ctypes.c_float] + [_vp] * 4 + [la, _vp, size, _vp, _vp], cint),
+                ("mamba_linattn_bwd", [_vp] * 4 + [ctypes.c_float] + [_vp] * 8 + [la, _vp, size, _vp, _vp], cint),
+                ("mamba_linattn_state_update", [_vp] * 5 + [ctypes.c_float, _vp, ctypes.POINTER(LinattnUpdateDims),
+                                                            _vp, _vp], cint),
+                ("mamba_gated_norm_fwd", [_vp] * 4 + [ctypes.POINTER(GatedNormDims), _vp, _vp], cint),
+                ("mamba_gated_norm_bwd_workspace_size", [ctypes.POINTER(GatedNormDims)], size),
+                ("mamba_gated_norm_bwd", [_vp] * 7 + [ctypes.POINTER(GatedNormDims), _vp, size, _vp, _vp], cint),
+                ("mamba_residual_norm_fwd", [_vp] * 6 + [ctypes.POINTER(ResidualNormDims), _vp, _vp], cint),
+                ("mamba_residual_norm_bwd_workspace_size", [ctypes.POINTER(ResidualNormDims)], size),
+                ("mamba_residual_norm_bwd", [_vp] * 10 + [ctypes.POINTER(ResidualNormDims), _vp, size, _vp, _vp], cint)):
+            getattr(lib, fn).argtypes, getattr(lib, fn).restype = args, res
         lib.mamba_status_string.argtypes = [ctypes.c_int]
         lib.mamba_status_string.restype = ctypes.c_char_p
         lib.mamba_debug_bounded_wait.argtypes = [ctypes.c_uint32, _vp, _vp]
@@ -267,6 +305,64 @@ def mamba_state_update(state, x, delta, A, B, C, D, z, delta_bias, softplus_flag
                        dims: UpdateDims, dev_status, stream) -> int:
     return library().mamba_state_update(state, x, delta, A, B, C, D, z, delta_bias,
                                         int(softplus_flag), y, ctypes.byref(dims), dev_status, stream)
+
+
+def mamba_linattn_workspace_size(dims: LinattnDims, packed: bool) -> int:
+    return library().mamba_linattn_workspace_size(ctypes.byref(dims), int(packed))
+
+
+def mamba_linattn_fwd(q, k, v, log_decay, scale, seq_start, initial_state, o, final_state, dims: LinattnDims, workspace,
+                      workspace_bytes, dev_status, stream) -> int:
+    return library().mamba_linattn_fwd(q, k, v, log_decay, scale, seq_start, initial_state, o, final_state,
+                                       ctypes.byref(dims), workspace, workspace_bytes, dev_status, stream)
+
+
+def mamba_linattn_bwd_workspace_size(dims: LinattnDims, packed: bool) -> int:
+    return library().mamba_linattn_bwd_workspace_size(ctypes.byref(dims), int(packed))
+
+
+def mamba_linattn_bwd(q, k, v, log_decay, scale, seq_start, initial_state, dout, dfinal, dq, dk, dv, dinitial_state,
+                      dims: LinattnDims, workspace, workspace_bytes, dev_status, stream) -> int:
+    return library().mamba_linattn_bwd(q, k, v, log_decay, scale, seq_start, initial_state, dout, dfinal, dq, dk, dv,
+                                       dinitial_state, ctypes.byref(dims), workspace, workspace_bytes, dev_status,
+                                       stream)
+
+
+def mamba_linattn_state_update(state, q, k, v, log_decay, scale, o, dims: LinattnUpdateDims, dev_status, stream) -> int:
+    return library().mamba_linattn_state_update(state, q, k, v, log_decay, scale, o, ctypes.byref(dims), dev_status,
+                                                stream)
+
+
+def mamba_gated_norm_fwd(x, z, weight, y, dims: GatedNormDims, dev_status, stream) -> int:
+    return library().mamba_gated_norm_fwd(x, z, weight, y, ctypes.byref(dims), dev_status, stream)
+
+
+def mamba_gated_norm_bwd_workspace_size(dims: GatedNormDims) -> int:
+    return library().mamba_gated_norm_bwd_workspace_size(ctypes.byref(dims))
+
+
+def mamba_gated_norm_bwd(x, z, weight, dy, dx, dz, dweight, dims: GatedNormDims, workspace, workspace_bytes,
+                         dev_status, stream) -> int:
+    return library().mamba_gated_norm_bwd(x, z, weight, dy, dx, dz, dweight, ctypes.byref(dims), workspace,
+                                          workspace_bytes, dev_status, stream)
+
+
+def mamba_residual_norm_fwd(x, residual, weight, channel_scale, y, residual_out, dims: ResidualNormDims, dev_status,
+                            stream) -> int:
+    return library().mamba_residual_norm_fwd(x, residual, weight, channel_scale, y, residual_out, ctypes.byref(dims),
+                                             dev_status, stream)
+
+
+def mamba_residual_norm_bwd_workspace_size(dims: ResidualNormDims) -> int:
+    return library().mamba_residual_norm_bwd_workspace_size(ctypes.byref(dims))
+
+
+def mamba_residual_norm_bwd(residual_out, weight, dy, dresidual_out, x, channel_scale, dx, dresidual, dweight,
+                            dchannel_scale, dims: ResidualNormDims, workspace, workspace_bytes, dev_status,
+                            stream) -> int:
+    return library().mamba_residual_norm_bwd(residual_out, weight, dy, dresidual_out, x, channel_scale, dx, dresidual,
+                                             dweight, dchannel_scale, ctypes.byref(dims), workspace, workspace_bytes,
+                                             dev_status, stream)
 
 
 # ----------------------------------------------------- torch conveniences ----
@@ -594,3 +690,277 @@ def state_update(state, x, delta, A, B, C, D=None, z=None, delta_bias=None, soft
     if rc != MS_OK:
         raise MambaScanError(rc, "mamba_state_update")
     return y
+
+
+# ------------------------------------------- linear attention and its norms ----
+
+def _layer_call(ref, stream, *others):
+    """The stream handle for a call on ``ref``'s device, every tensor checked
+    to be on that device and the device to be the current one (the library
+    launches on the current device)."""
+    torch = _torch()
+    dev = ref.device
+    if dev.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but cuda:{torch.cuda.current_device()} is the current device")
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _same_type(t, shape, dtype, name):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or (t.numel() > 0 and t.stride(-1) != 1)):
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} with unit stride along its last dimension")
+
+
+def _dense_f32(t, shape, name):
+    torch = _torch()
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != torch.float32 or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {tuple(shape)}")
+
+
+def _workspace(ws, need, device):
+    """A caller's workspace, or one allocated for the call: (tensor or None, address, bytes)."""
+    torch = _torch()
+    if ws is None:
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def linattn_dims_for(q, k, v, o, seq_start=None) -> LinattnDims:
+    """LinattnDims read off q/k/v/o [b, L, heads, d], or [rows, heads, d] with
+    seq_start."""
+    if seq_start is not None:
+        total, H, dk = q.shape
+        n = seq_start.shape[0] - 1
+        qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
+        return LinattnDims(n, 0, total, H, k.shape[1], dk, v.shape[2], 0, qs[0], qs[1], 0, ks[0], ks[1], 0, vs[0],
+                           vs[1], 0, os_[0], os_[1], _dtype_code(q))
+    b, L, H, dk = q.shape
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
+    return LinattnDims(b, L, 0, H, k.shape[2], dk, v.shape[3], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1],
+                       vs[2], os_[0], os_[1], os_[2], _dtype_code(q))
+
+
+def _check_linattn(q, k, v, log_decay, seq_start):
+    torch = _torch()
+    want = 4 if seq_start is None else 3
+    if q.dim() != want or k.dim() != want or v.dim() != want:
+        raise ValueError(f"q, k, v must have {want} dimensions")
+    lead, H, dk, G = q.shape[:-2], q.shape[-2], q.shape[-1], k.shape[-2]
+    _same_type(q, q.shape, q.dtype, "q")
+    _same_type(k, (*lead, G, dk), q.dtype, "k")
+    _same_type(v, (*lead, G, v.shape[-1]), q.dtype, "v")
+    _dense_f32(log_decay, (H,), "log_decay")
+    if seq_start is None:
+        return q.shape[0], H, dk, v.shape[-1], (*lead, H, v.shape[-1])
+    if seq_start.dtype != torch.int32 or seq_start.dim() != 1 or seq_start.shape[0] < 1 or not seq_start.is_contiguous():
+        raise ValueError("seq_start must be a contiguous int32 tensor of shape (sequences + 1,)")
+    return seq_start.shape[0] - 1, H, dk, v.shape[-1], (*lead, H, v.shape[-1])
+
+
+def linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, seq_start=None, initial_state=None, o=None,
+                final_state=None, return_final_state: bool = True, stream=None, dev_status=None, workspace=None):
+    """Linear attention with a decay per head over whole sequences (see
+    include/mambascan.h, mamba_linattn_fwd): q [b, L, H, dk], k [b, L, G, dk],
+    v [b, L, G, dv] in bf16 or fp32, log_decay [H] fp32; with ``seq_start``
+    (int32 CUDA tensor [sequences + 1]) the tensors are [rows, heads, d] and
+    rows of no sequence keep what ``o`` held. ``scale`` None = dk ** -0.5.
+    ``final_state`` may be ``initial_state``. ``workspace`` (uint8 CUDA tensor
+    of at least ``mamba_linattn_workspace_size`` bytes) is allocated per call
+    when omitted. Returns (o, final_state or None)."""
+    torch = _torch()
+    n, H, dk, dv, oshape = _check_linattn(q, k, v, log_decay, seq_start)
+    if o is None:
+        o = torch.empty(oshape, dtype=q.dtype, device=q.device)
+    else:
+        _same_type(o, oshape, q.dtype, "o")
+    fs = final_state
+    if fs is None and return_final_state:
+        fs = torch.empty((n, H, dk, dv), dtype=torch.float32, device=q.device)
+    _dense_f32(initial_state, (n, H, dk, dv), "initial_state")
+    _dense_f32(final_state, (n, H, dk, dv), "final_state")
+    st = _layer_call(q, stream, k, v, log_decay, seq_start, initial_state, o, fs, dev_status, workspace)
+    dims = linattn_dims_for(q, k, v, o, seq_start)
+    ws, wp, wb = _workspace(workspace, mamba_linattn_workspace_size(dims, seq_start is not None), q.device)
+    rc = mamba_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), dk ** -0.5 if scale is None else scale,
+                           _ptr(seq_start), _ptr(initial_state), _ptr(o), _ptr(fs), dims, wp, wb, _ptr(dev_status), st)
+    if rc != MS_OK:
+        raise MambaScanError(rc, "mamba_linattn_fwd")
+    return o, fs
+
+
+def linattn_bwd(q, k, v, log_decay, dout, scale: Optional[float] = None, seq_start=None, initial_state=None,
+                dfinal=None, want_dinitial: bool = True, grads=None, stream=None, dev_status=None, workspace=None):
+    """Gradients of linattn_fwd for dL/do = dout and dL/dfinal_state = dfinal:
+    a dict dq, dk, dv (types and layouts of q, k, v) and dinitial_state (fp32,
+    None unless wanted). ``grads`` may hold preallocated dq, dk, dv with the
+    strides of q, k, v (rows of no sequence keep what they held)."""
+    torch = _torch()
+    n, H, dk, dv, oshape = _check_linattn(q, k, v, log_decay, seq_start)
+    _same_type(dout, oshape, q.dtype, "dout")
+    _dense_f32(initial_state, (n, H, dk, dv), "initial_state")
+    _dense_f32(dfinal, (n, H, dk, dv), "dfinal")
+    g = {}
+    for name, t in (("dq", q), ("dk", k), ("dv", v)):
+        got = None if grads is None else grads.get(name)
+        if got is None:
+            got = torch.empty_strided(t.shape, t.stride(), dtype=t.dtype, device=t.device)
+        elif got.shape != t.shape or got.dtype != t.dtype or got.stride() != t.stride():
+            raise ValueError(f"{name} must have the shape, type and strides of {name[1]}")
+        g[name] = got
+    g["dinitial_state"] = torch.empty((n, H, dk, dv), dtype=torch.float32, device=q.device) if want_dinitial else None
+    st = _layer_call(q, stream, k, v, log_decay, seq_start, initial_state, dout, dfinal, g["dq"], g["dk"], g["dv"],
+                     dev_status, workspace)
+    dims = linattn_dims_for(q, k, v, dout, seq_start)
+    ws, wp, wb = _workspace(workspace, mamba_linattn_bwd_workspace_size(dims, seq_start is not None), q.device)
+    rc = mamba_linattn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), dk ** -0.5 if scale is None else scale,
+                           _ptr(seq_start), _ptr(initial_state), _ptr(dout), _ptr(dfinal), _ptr(g["dq"]),
+                           _ptr(g["dk"]), _ptr(g["dv"]), _ptr(g["dinitial_state"]), dims, wp, wb, _ptr(dev_status), st)
+    if rc != MS_OK:
+        raise MambaScanError(rc, "mamba_linattn_bwd")
+    return g
+
+
+def linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] = None, o=None, stream=None,
+                         dev_status=None):
+    """One token of linattn_fwd: state [b, H, dk, dv] fp32 (dense [dk, dv]
+    blocks, updated in place), q [b, H, dk], k [b, G, dk], v [b, G, dv].
+    Returns o [b, H, dv]."""
+    torch = _torch()
+    b, H, dk = q.shape
+    G, dv = v.shape[1], v.shape[2]
+    if state.shape != (b, H, dk, dv) or state.dtype != torch.float32 or state.stride()[2:] != (dv, 1):
+        raise ValueError(f"state must be {(b, H, dk, dv)} fp32 with dense [dk, dv] blocks")
+    _same_type(q, q.shape, q.dtype, "q")
+    _same_type(k, (b, G, dk), q.dtype, "k")
+    _same_type(v, (b, G, dv), q.dtype, "v")
+    _dense_f32(log_decay, (H,), "log_decay")
+    if o is None:
+        o = torch.empty((b, H, dv), dtype=q.dtype, device=q.device)
+    else:
+        _same_type(o, (b, H, dv), q.dtype, "o")
+    st = _layer_call(state, stream, q, k, v, log_decay, o, dev_status)
+    qs, ks, vs, os_, ss = q.stride(), k.stride(), v.stride(), o.stride(), state.stride()
+    dims = LinattnUpdateDims(b, H, G, dk, dv, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], ss[0], ss[1],
+                             _dtype_code(q))
+    rc = mamba_linattn_state_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                    dk ** -0.5 if scale is None else scale, _ptr(o), dims, _ptr(dev_status), st)
+    if rc != MS_OK:
+        raise MambaScanError(rc, "mamba_linattn_state_update")
+    return o
+
+
+def _rows(t, name, shape=None, dtype=None):
+    if t is None:
+        return 0
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, width]")
+    if shape is not None:
+        _same_type(t, shape, dtype, name)
+    return t.stride(0)
+
+
+def gated_norm_fwd(x, z=None, weight=None, groups: int = 1, eps: float = 1e-5, gate_first: bool = False, y=None,
+                   stream=None, dev_status=None):
+    """Gated group norm (see include/mambascan.h, mamba_gated_norm_fwd) of x
+    [rows, width]: norm(x) w silu(z), or norm(x silu(z)) w with
+    ``gate_first``. Returns y."""
+    torch = _torch()
+    xs = _rows(x, "x", x.shape, x.dtype)
+    zs = _rows(z, "z", x.shape, x.dtype)
+    _dense_f32(weight, x.shape[1:], "weight")
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    st = _layer_call(x, stream, z, weight, y, dev_status)
+    dims = GatedNormDims(x.shape[0], x.shape[1], groups, xs, zs, _rows(y, "y", x.shape, x.dtype), eps, _dtype_code(x),
+                         int(gate_first))
+    rc = mamba_gated_norm_fwd(_ptr(x), _ptr(z), _ptr(weight), _ptr(y), dims, _ptr(dev_status), st)
+    if rc != MS_OK:
+        raise MambaScanError(rc, "mamba_gated_norm_fwd")
+    return y
+
+
+def gated_norm_bwd(x, z, weight, dy, groups: int = 1, eps: float = 1e-5, gate_first: bool = False,
+                   want_dweight: bool = True, stream=None, dev_status=None, workspace=None):
+    """Gradients of gated_norm_fwd: a dict dx, dz (None without z), dweight
+    (fp32; None unless wanted)."""
+    torch = _torch()
+    xs = _rows(x, "x", x.shape, x.dtype)
+    zs = _rows(z, "z", x.shape, x.dtype)
+    _dense_f32(weight, x.shape[1:], "weight")
+    g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
+         "dz": torch.empty(x.shape, dtype=x.dtype, device=x.device) if z is not None else None,
+         "dweight": torch.empty(x.shape[1], dtype=torch.float32, device=x.device) if want_dweight else None}
+    st = _layer_call(x, stream, z, weight, dy, dev_status, workspace)
+    dims = GatedNormDims(x.shape[0], x.shape[1], groups, xs, zs, _rows(dy, "dy", x.shape, x.dtype), eps,
+                         _dtype_code(x), int(gate_first))
+    ws, wp, wb = _workspace(workspace, mamba_gated_norm_bwd_workspace_size(dims) if want_dweight else 0, x.device)
+    rc = mamba_gated_norm_bwd(_ptr(x), _ptr(z), _ptr(weight), _ptr(dy), _ptr(g["dx"]), _ptr(g["dz"]),
+                              _ptr(g["dweight"]), dims, wp, wb, _ptr(dev_status), st)
+    if rc != MS_OK:
+        raise MambaScanError(rc, "mamba_gated_norm_bwd")
+    return g
+
+
+def residual_norm_fwd(x, residual=None, weight=None, eps: float = 1e-5, res_scale: float = 1.0, channel_scale=None,
+                      y=None, residual_out=None, residual_dtype=None, stream=None, dev_status=None):
+    """Residual add and norm (see include/mambascan.h,
+    mamba_residual_norm_fwd): residual_out = residual + res_scale
+    channel_scale x, y = norm(residual_out) weight. ``residual_out`` (of the
+    residual's type, else of ``residual_dtype``, else x's) may be
+    ``residual``. Returns (y, residual_out)."""
+    torch = _torch()
+    xs = _rows(x, "x", x.shape, x.dtype)
+    rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else \
+        residual_dtype or x.dtype
+    if residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=rt, device=x.device)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _dense_f32(weight, x.shape[1:], "weight")
+    _dense_f32(channel_scale, x.shape[1:], "channel_scale")
+    st = _layer_call(x, stream, residual, weight, channel_scale, y, residual_out, dev_status)
+    dims = ResidualNormDims(x.shape[0], x.shape[1], xs, _rows(residual, "residual", x.shape, rt),
+                            _rows(y, "y", x.shape, x.dtype), _rows(residual_out, "residual_out", x.shape, rt), eps,
+                            res_scale, _dtype_code(x), _dtype_code(residual_out))
+    rc = mamba_residual_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(channel_scale), _ptr(y),
+                                 _ptr(residual_out), dims, _ptr(dev_status), st)
+    if rc != MS_OK:
+        raise MambaScanError(rc, "mamba_residual_norm_fwd")
+    return y, residual_out
+
+
+def residual_norm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, eps: float = 1e-5, res_scale: float = 1.0,
+                      channel_scale=None, want_dweight: bool = True, stream=None, dev_status=None, workspace=None):
+    """Gradients of residual_norm_fwd from its sum ``residual_out``: a dict dx
+    (dy's type), dresidual (the sum's type), dweight and, where x and
+    channel_scale are given, dchannel_scale (fp32)."""
+    torch = _torch()
+    shape = dy.shape
+    rs = _rows(residual_out, "residual_out", shape, residual_out.dtype)
+    _dense_f32(weight, shape[1:], "weight")
+    _dense_f32(channel_scale, shape[1:], "channel_scale")
+    with_c = x is not None and channel_scale is not None
+    f32 = dict(dtype=torch.float32, device=dy.device)
+    g = {"dx": torch.empty(shape, dtype=dy.dtype, device=dy.device),
+         "dresidual": torch.empty(shape, dtype=residual_out.dtype, device=dy.device),
+         "dweight": torch.empty(shape[1], **f32) if want_dweight else None,
+         "dchannel_scale": torch.empty(shape[1], **f32) if with_c else None}
+    st = _layer_call(dy, stream, residual_out, weight, dresidual_out, x, channel_scale, dev_status, workspace)
+    dims = ResidualNormDims(shape[0], shape[1], _rows(x, "x", shape, dy.dtype),
+                            _rows(dresidual_out, "dresidual_out", shape, residual_out.dtype),
+                            _rows(dy, "dy", shape, dy.dtype), rs, eps, res_scale, _dtype_code(dy),
+                            _dtype_code(residual_out))
+    need = mamba_residual_norm_bwd_workspace_size(dims) if want_dweight or with_c else 0
+    ws, wp, wb = _workspace(workspace, need, dy.device)
+    rc = mamba_residual_norm_bwd(_ptr(residual_out), _ptr(weight), _ptr(dy), _ptr(dresidual_out), _ptr(x),
+                                 _ptr(channel_scale), _ptr(g["dx"]), _ptr(g["dresidual"]), _ptr(g["dweight"]),
+                                 _ptr(g["dchannel_scale"]), dims, wp, wb, _ptr(dev_status), st)
+    if rc != MS_OK:
+        raise MambaScanError(rc, "mamba_residual_norm_bwd")
+    return g

@@ -1,0 +1,250 @@
+// linattn_plain.cu -- linear attention with a decay per head as the plain
+// recurrence, the sum of shared heads' gradients, and the one-token update.
+
+#include <cstdint>
+
+#include "mambascan.h"
+#include "ms_device.cuh"
+#include "ms_internal.h"
+
+namespace ms {
+
+namespace {
+
+// lam S + c as keep S + (part S + c). For lam >= 1/2 keep = 1 and part = lam - 1, which
+// keeps the bits of a slow decay: lam itself rounded to fp32 is up to 2^-25 off, which
+// 4096 remembered tokens would make 2^-13 of the state. Below, keep = 0 and part = lam,
+// so that what is forgotten leaves no rounding behind.
+struct Decay {
+    float keep, part;
+};
+__device__ __forceinline__ Decay decay_of(float log_decay) {
+    const float m = expm1f(log_decay);
+    return m >= -0.5f ? Decay{1.0f, m} : Decay{0.0f, expf(log_decay)};
+}
+__device__ __forceinline__ float decayed(float s, const Decay &d, float c) {
+    return fmaf(d.keep, s, fmaf(d.part, s, c));
+}
+
+constexpr int kPT = 16;    // tokens staged at a time
+constexpr int kPThr = 128; // one thread per column of the state
+
+// The tokens of sequence i: offset of its first row inside the arrays (packed)
+// and its length; false where the caller's offsets are not in order.
+__device__ __forceinline__ bool seq_rows(const int32_t *seq_start, int64_t total, int64_t seqlen, int64_t i,
+                                         int64_t &row0, int64_t &len) {
+    if (seq_start == nullptr) {
+        row0 = 0;
+        len = seqlen;
+        return true;
+    }
+    const int64_t s = seq_start[i], e = seq_start[i + 1];
+    row0 = s;
+    len = e - s;
+    return s >= 0 && e >= s && e <= total;
+}
+
+// One CTA per (sequence, head, problem); thread e holds column e of the state,
+// all dx rows of it, in registers. Per token 3 dx multiply-adds a thread: the
+// FMA pipe bounds it. It serves the sizes, types and alignments that the
+// tensor-core kernel does not take.
+template <typename T, int DX>
+__global__ void __launch_bounds__(kPThr) linattn_plain_kernel(const LaArgs a) {
+    const LaProblem &p = a.p[blockIdx.y];
+    const int64_t b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const int e = threadIdx.x;
+    __shared__ __align__(16) float xs[kPT][DX], ys[kPT][DX];
+    int64_t row0, len;
+    if (!seq_rows(a.seq_start, a.total, a.seqlen, b, row0, len)) {
+        if (e == 0 && a.status) atomicOr(a.status, MS_ERR_SHAPE);
+        return;
+    }
+    const int64_t bs = a.seq_start ? 0 : b;
+    const T *x = static_cast<const T *>(p.x) + bs * p.x_sb + row0 * p.x_sl + (h / p.xg) * p.x_sh;
+    const T *y = static_cast<const T *>(p.y) + bs * p.y_sb + row0 * p.y_sl + (h / p.yg) * p.y_sh;
+    const T *z = static_cast<const T *>(p.z) + bs * p.z_sb + row0 * p.z_sl + (h / p.zg) * p.z_sh;
+    const int64_t o0 = bs * p.o_sb + row0 * p.o_sl + h * p.o_sh;
+    const Decay lam = decay_of(__ldg(a.log_decay + h));
+    const bool live = e < p.dz;
+    float S[DX];
+    const float *s0 = p.s0 ? p.s0 + (b * a.H + h) * p.dx * p.dz : nullptr;
+#pragma unroll
+    for (int i = 0; i < DX; ++i) S[i] = (s0 && live && i < p.dx) ? s0[i * p.s0_sr + e * p.s0_sc] : 0.0f;
+    for (int64_t c = 0; c < len; c += kPT) {
+        const int n = (int)(len - c < kPT ? len - c : kPT);
+        __syncthreads();
+        for (int i = e; i < kPT * DX; i += kPThr) {
+            const int t = i / DX, d = i % DX;
+            const bool in = t < n && d < p.dx;
+            const int64_t tok = p.rev ? len - 1 - c - t : c + t;
+            xs[t][d] = in ? Elem<T>::load(x + tok * p.x_sl + d) : 0.0f;
+            ys[t][d] = in ? Elem<T>::load(y + tok * p.y_sl + d) : 0.0f;
+        }
+        __syncthreads();
+        for (int t = 0; t < n; ++t) {
+            const int64_t tok = p.rev ? len - 1 - c - t : c + t;
+            const float zt = live ? p.ws * Elem<T>::load(z + tok * p.z_sl + e) : 0.0f;
+            // forward order decays before the token, reverse order after it (here: before the
+            // next one, and once more at the end)
+            const Decay pre = (p.rev && c + t == 0) ? Decay{1.0f, 0.0f} : lam;
+            float acc = 0.0f;
+#pragma unroll
+            for (int i = 0; i < DX; ++i) {
+                S[i] = decayed(S[i], pre, ys[t][i] * zt);
+                acc = fmaf(xs[t][i], S[i], acc);
+            }
+            if (live) {
+                const int64_t at = o0 + tok * p.o_sl + e;
+                if (p.o_f32) static_cast<float *>(p.o)[at] = p.ro * acc;
+                else Elem<T>::store(static_cast<T *>(p.o) + at, p.ro * acc);
+            }
+        }
+    }
+    if (p.fin && live) {
+        float *f = p.fin + (b * a.H + h) * p.dx * p.dz + e;
+        const Decay post = (p.rev && len > 0) ? lam : Decay{1.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < DX; ++i)
+            if (i < p.dx) f[(int64_t)i * p.dz] = decayed(S[i], post, 0.0f);
+    }
+}
+
+template <typename T>
+cudaError_t launch_plain_t(const LaArgs &a, cudaStream_t stream) {
+    int dx = 1;
+    for (int i = 0; i < a.np; ++i) dx = a.p[i].dx > dx ? a.p[i].dx : dx;
+    const int64_t blocks = a.batch * a.H;
+    if (blocks <= 0) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)blocks, (unsigned)a.np);
+    if (dx <= 32) linattn_plain_kernel<T, 32><<<grid, kPThr, 0, stream>>>(a);
+    else if (dx <= 64) linattn_plain_kernel<T, 64><<<grid, kPThr, 0, stream>>>(a);
+    else linattn_plain_kernel<T, 128><<<grid, kPThr, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+// out[row][g][i] = sum of part[row][h][i] over the heads h of g, in their order.
+template <typename T>
+__global__ void __launch_bounds__(256) linattn_reduce_kernel(const LaReduceArgs a) {
+    const int64_t per = a.kv * a.d, n = a.H / a.kv;
+    int64_t first = 0, rows = a.batch * a.seqlen;
+    if (a.seq_start) {
+        const int64_t s = a.seq_start[0], e = a.seq_start[a.batch];
+        first = s < 0 ? 0 : s;
+        rows = (e < a.total ? e : a.total) - first;
+    }
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = first + i / per, g = i % per / a.d, c = i % a.d;
+        const float *src = a.part + (row * a.H + g * n) * a.d + c;
+        float s = 0.0f;
+        for (int64_t j = 0; j < n; ++j) s += src[j * a.d];
+        const int64_t b = a.seq_start ? 0 : row / a.seqlen, t = a.seq_start ? row : row % a.seqlen;
+        Elem<T>::store(static_cast<T *>(a.out) + b * a.o_sb + t * a.o_sl + g * a.o_sh + c, s);
+    }
+}
+
+// ------------------------------------------------------------ one token ----
+
+constexpr int kUThr = 256;
+
+// S = lam S + k v^T and o = a q S for one (row, head): the state is read and
+// written once, which bounds it (HBM). A thread owns VEC neighbouring columns
+// and every rp-th row; its first kURows loads are in flight together; the
+// column sums of q S meet in shared memory.
+constexpr int kURows = 8;
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kUThr) linattn_update_kernel(const LaUpdateArgs a, int cg) {
+    const int64_t b = blockIdx.x / a.H, h = blockIdx.x % a.H, g = h / (a.H / a.kv);
+    const int col = threadIdx.x % cg, r0 = threadIdx.x / cg, rp = kUThr / cg;
+    const int e0 = col * VEC;
+    __shared__ float red[kUThr * VEC];
+    const T *q = static_cast<const T *>(a.q) + b * a.q_sb + h * a.q_sh;
+    const T *k = static_cast<const T *>(a.k) + b * a.k_sb + g * a.k_sh;
+    const T *v = static_cast<const T *>(a.v) + b * a.v_sb + g * a.v_sh;
+    float *st = a.state + b * a.st_sb + h * a.st_sh + e0;
+    const bool live = e0 < a.dv;
+    const Decay lam = decay_of(__ldg(a.log_decay + h));
+    float acc[VEC], vv[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+        acc[j] = 0.0f;
+        vv[j] = live ? Elem<T>::load(v + e0 + j) : 0.0f;
+    }
+    for (int i0 = r0; live && i0 < a.dk; i0 += rp * kURows) {
+        float s[kURows][VEC], kk[kURows], qq[kURows];
+#pragma unroll
+        for (int u = 0; u < kURows; ++u) {
+            const int i = i0 + u * rp;
+            if (i < a.dk) {
+                if constexpr (VEC == 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(st + (int64_t)i * a.dv);
+                    s[u][0] = t.x; s[u][1] = t.y; s[u][2] = t.z; s[u][3] = t.w;
+                } else {
+                    s[u][0] = st[(int64_t)i * a.dv];
+                }
+                kk[u] = Elem<T>::load(k + i);
+                qq[u] = Elem<T>::load(q + i);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kURows; ++u) {
+            const int i = i0 + u * rp;
+            if (i < a.dk) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    s[u][j] = decayed(s[u][j], lam, kk[u] * vv[j]);
+                    acc[j] = fmaf(qq[u], s[u][j], acc[j]);
+                }
+                if constexpr (VEC == 4)
+                    *reinterpret_cast<float4 *>(st + (int64_t)i * a.dv) = make_float4(s[u][0], s[u][1], s[u][2], s[u][3]);
+                else
+                    st[(int64_t)i * a.dv] = s[u][0];
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) red[r0 * cg * VEC + e0 + j] = acc[j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.dv; e += kUThr) {
+        float s = 0.0f;
+        for (int r = 0; r < rp; ++r) s += red[r * cg * VEC + e];
+        Elem<T>::store(static_cast<T *>(a.o) + b * a.o_sb + h * a.o_sh + e, a.scale * s);
+    }
+}
+
+template <typename T>
+cudaError_t launch_update_t(const LaUpdateArgs &a, cudaStream_t stream) {
+    const int64_t blocks = a.batch * a.H;
+    if (blocks <= 0) return cudaSuccess;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const bool vec = a.dv % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0 && a.st_sb % 4 == 0 && a.st_sh % 4 == 0;
+    const int cols = vec ? a.dv / 4 : a.dv;
+    int cg = 1;
+    while (cg < cols) cg *= 2;
+    if (cg > kUThr) return cudaErrorInvalidConfiguration;
+    if (vec) linattn_update_kernel<T, 4><<<(unsigned)blocks, kUThr, 0, stream>>>(a, cg);
+    else linattn_update_kernel<T, 1><<<(unsigned)blocks, kUThr, 0, stream>>>(a, cg);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linattn_plain(const LaArgs &a, bool bf16, cudaStream_t stream) {
+    return bf16 ? launch_plain_t<__nv_bfloat16>(a, stream) : launch_plain_t<float>(a, stream);
+}
+
+cudaError_t launch_linattn_reduce(const LaReduceArgs &a, bool bf16, cudaStream_t stream) {
+    const int64_t n = (a.seq_start ? a.total : a.batch * a.seqlen) * a.kv * a.d;
+    if (n <= 0) return cudaSuccess;
+    const int64_t want = (n + 255) / 256;
+    const unsigned grid = (unsigned)(want < 148 * 16 ? want : 148 * 16);
+    if (bf16) linattn_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
+    else linattn_reduce_kernel<float><<<grid, 256, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linattn_update(const LaUpdateArgs &a, bool bf16, cudaStream_t stream) {
+    return bf16 ? launch_update_t<__nv_bfloat16>(a, stream) : launch_update_t<float>(a, stream);
+}
+
+}  // namespace ms

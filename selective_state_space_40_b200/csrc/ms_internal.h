@@ -132,6 +132,85 @@ struct SsdUpdArgs {
 };
 cudaError_t launch_ssd_update(const SsdUpdArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream);
 
+// One direction of linear attention with a decay per head. Forward, and each
+// gradient, is the same map of three token arrays x, y [., dx] and z [., dz]
+// (rev: over the tokens from the last to the first):
+//   S = lam S + ws y_t z_t^T,   o_t = ro x_t S        (forward order: x, y, z = q, k, v)
+//   o_t = ro x_t R,  R = ws y_t z_t^T + lam R_next    (rev: the decay follows the token)
+// dq: x, y, z = dout, v, k; dk: v, dout, q (rev); dv: k, q, dout (rev).
+struct LaProblem {
+    const void *x, *y, *z;
+    void *o;
+    const float *s0;  // entering state or null; element (i, j) of a head's block at i * s0_sr + j * s0_sc
+    float *fin;       // leaving state or null, [batch, H, dx, dz] dense
+    int64_t x_sb, x_sl, x_sh, y_sb, y_sl, y_sh, z_sb, z_sl, z_sh, o_sb, o_sl, o_sh;
+    int64_t s0_sr, s0_sc;
+    int xg, yg, zg;   // heads that share one head of x, y, z
+    int dx, dz;
+    int rev, o_f32;
+    float ws, ro;
+};
+constexpr int kLaMaxProblems = 3;
+struct LaArgs {
+    const float *log_decay;
+    const int32_t *seq_start;  // null: dense [batch, seqlen]
+    int *status;
+    int64_t batch, seqlen, total, H;
+    LaProblem p[kLaMaxProblems];
+    int np;
+};
+// The plain recurrence (any sizes up to 128, strides and alignment, bf16 or fp32).
+cudaError_t launch_linattn_plain(const LaArgs &a, bool bf16, cudaStream_t stream);
+// Sums the fp32 rows part [rows, H, d] over the H / kv heads that share a kv
+// head into out [row, kv, d] (rows as the problem's tokens lie).
+struct LaReduceArgs {
+    const float *part;
+    void *out;
+    const int32_t *seq_start;
+    int64_t batch, seqlen, total, H, kv, d;
+    int64_t o_sb, o_sl, o_sh;
+};
+cudaError_t launch_linattn_reduce(const LaReduceArgs &a, bool bf16, cudaStream_t stream);
+
+struct LaUpdateArgs {
+    float *state;
+    const void *q, *k, *v;
+    const float *log_decay;
+    void *o;
+    int *status;
+    int64_t batch, H, kv;
+    int dk, dv;
+    int64_t q_sb, q_sh, k_sb, k_sh, v_sb, v_sh, o_sb, o_sh, st_sb, st_sh;
+    float scale;
+};
+cudaError_t launch_linattn_update(const LaUpdateArgs &a, bool bf16, cudaStream_t stream);
+
+// Norms (norms.cu). part: partial sums over rows, [parts, width] fp32 per weight.
+struct GatedNormArgs {
+    const void *x, *z, *dy;
+    const float *w;
+    void *y, *dx, *dz;
+    float *dw, *part;
+    int *status;
+    int64_t rows, width, groups, x_sr, z_sr, y_sr;
+    float eps;
+    int gate_first;
+};
+struct ResidualNormArgs {
+    const void *x, *res, *dy, *dres_out;
+    const float *w, *cs;
+    void *y, *res_out, *dx, *dres;
+    float *dw, *dcs, *part;
+    int *status;
+    int64_t rows, width, x_sr, res_sr, y_sr, ro_sr;
+    float eps, scale;
+};
+constexpr int64_t kNormMaxWidth = 16384;
+size_t norm_parts(int64_t rows, int64_t width, int64_t groups, int num_sms);
+cudaError_t launch_gated_norm(const GatedNormArgs &a, bool bf16, bool bwd, int num_sms, cudaStream_t stream);
+cudaError_t launch_residual_norm(const ResidualNormArgs &a, bool bf16, bool res_bf16, bool bwd, int num_sms,
+                                 cudaStream_t stream);
+
 // Launch shape chosen on the host for one scan call.
 struct ScanPlan {
     int lanes_per_channel;  // G: lanes sharing one channel (1, 2, 4, 8), 16/G states each
