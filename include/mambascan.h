@@ -415,7 +415,9 @@ int mamba2_ssd_state_update(float *state, const void *x, const void *dt, const f
  * seq_start[i+1] - 1 of `total` rows; seqlen and the *_sb strides are not
  * read. Lengths may be 0, and rows of no sequence are neither read nor
  * written. A sequence whose rows are not within [0, total] in order is left
- * out and MS_ERR_SHAPE is ORed into dev_status.
+ * out and MS_ERR_SHAPE is ORed into dev_status; where the offsets decrease,
+ * the other sequences' results are undefined too (nothing outside the arrays
+ * is touched).
  * dk and dv are 1..128, all arrays of one type, bf16 or fp32. bf16 rows that
  * start on 16-byte boundaries (every pointer and stride) with dk and dv
  * multiples of 8 run on the tcgen05 tensor cores in chunks of 128 tokens:

@@ -121,14 +121,27 @@ size_t shared_bytes(const ms_linattn_dims *d, int64_t width, bool packed) {
     return round256(rows * (size_t)d->nheads * (size_t)width * sizeof(float));
 }
 
+// States between segments on the tensor-core path (needed by any bf16 call of
+// these sizes, so that the size does not depend on pointers and strides).
+size_t state_bytes(const ms_linattn_dims *d, bool packed, bool bwd) {
+    if (!d || d->dtype != MS_BF16 || d->batch < 1 || d->nheads < 1 || d->seqlen < 0 || d->total < 0 || d->dk < 1 ||
+        d->dk > 128 || d->dv < 1 || d->dv > 128)
+        return 0;
+    return round256(ms::linattn_tc_workspace(d->batch, packed ? d->total : d->seqlen, packed, d->nheads, (int)d->dk,
+                                             (int)d->dv, bwd, num_sms_current()));
+}
+
+cudaError_t launch_linattn(const ms::LaArgs &a, bool bf16, void *states, cudaStream_t st) {
+    return ms::linattn_tc_applies(a, bf16) ? ms::launch_linattn_tc(a, states, num_sms_current(), st)
+                                           : ms::launch_linattn_plain(a, bf16, st);
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t mamba_linattn_workspace_size(const ms_linattn_dims *d, int packed) {
-    (void)packed;
-    if (!d) return 0;
-    return 0;
+    return state_bytes(d, packed != 0, false);
 }
 
 int mamba_linattn_fwd(const void *q, const void *k, const void *v, const float *log_decay, float scale,
@@ -150,12 +163,12 @@ int mamba_linattn_fwd(const void *q, const void *k, const void *v, const float *
     a.p[0] = la_problem(Tok{q, d->q_sb, d->q_sl, d->q_sh, 1, dk}, Tok{k, d->k_sb, d->k_sl, d->k_sh, share, dk},
                         Tok{v, d->v_sb, d->v_sl, d->v_sh, share, dv}, Tok{o, d->o_sb, d->o_sl, d->o_sh, 1, dv},
                         initial_state, false, final_state, false, scale);
-    return cuda_rc(ms::launch_linattn_plain(a, d->dtype == MS_BF16, (cudaStream_t)stream));
+    return cuda_rc(launch_linattn(a, d->dtype == MS_BF16, workspace, (cudaStream_t)stream));
 }
 
 size_t mamba_linattn_bwd_workspace_size(const ms_linattn_dims *d, int packed) {
     if (!d || d->batch < 1 || d->nheads < 1 || d->kv_heads < 1 || d->seqlen < 0 || d->total < 0) return 0;
-    return shared_bytes(d, d->dk, packed != 0) + shared_bytes(d, d->dv, packed != 0);
+    return shared_bytes(d, d->dk, packed != 0) + shared_bytes(d, d->dv, packed != 0) + state_bytes(d, packed != 0, true);
 }
 
 int mamba_linattn_bwd(const void *q, const void *k, const void *v, const float *log_decay, float scale,
@@ -186,14 +199,13 @@ int mamba_linattn_bwd(const void *q, const void *k, const void *v, const float *
         gk = Tok{ws, d->seqlen * H * dk, H * dk, dk, 1, dk};
         gv = Tok{ws + pk, d->seqlen * H * dv, H * dv, dv, 1, dv};
     }
-    (void)pv;
     ms::LaArgs a = la_args(d, log_decay, seq_start, dev_status);
     a.np = 3;
     a.p[0] = la_problem(to, tv, tk, gq, initial_state, true, nullptr, false, scale);
     a.p[1] = la_problem(tv, to, tq, gk, dfinal, true, nullptr, true, scale);
     a.p[2] = la_problem(tk, tq, to, gv, dfinal, false, dinitial_state, true, scale);
     a.p[1].o_f32 = a.p[2].o_f32 = share > 1 ? 1 : 0;
-    cudaError_t e = ms::launch_linattn_plain(a, bf16, st);
+    cudaError_t e = launch_linattn(a, bf16, ws + pk + pv, st);
     if (e == cudaSuccess && share > 1) {
         ms::LaReduceArgs r{};
         r.seq_start = seq_start;

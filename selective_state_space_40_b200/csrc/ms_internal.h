@@ -161,6 +161,11 @@ struct LaArgs {
 };
 // The plain recurrence (any sizes up to 128, strides and alignment, bf16 or fp32).
 cudaError_t launch_linattn_plain(const LaArgs &a, bool bf16, cudaStream_t stream);
+// The same in chunks on the tensor cores: whether these sizes, strides and
+// pointers allow it, the workspace it needs (whether it applies or not), and the launch.
+bool linattn_tc_applies(const LaArgs &a, bool bf16);
+size_t linattn_tc_workspace(int64_t batch, int64_t rows, bool packed, int64_t H, int dk, int dv, bool bwd, int num_sms);
+cudaError_t launch_linattn_tc(const LaArgs &a, void *workspace, int num_sms, cudaStream_t stream);
 // Sums the fp32 rows part [rows, H, d] over the H / kv heads that share a kv
 // head into out [row, kv, d] (rows as the problem's tokens lie).
 struct LaReduceArgs {
