@@ -50,7 +50,7 @@ int check_linattn(const ms_linattn_dims *d, bool packed, const void *const *tok,
         d->v_sl < 0 || d->v_sh < 0 || d->o_sb < 0 || d->o_sl < 0 || d->o_sh < 0)
         return MS_ERR_STRIDE;
     const int64_t rows = packed ? d->total : d->seqlen, nb = packed ? 1 : (d->batch < 1 ? 1 : d->batch);
-    if (rows > INT32_MAX || d->batch > INT32_MAX) return MS_ERR_SHAPE;
+    if (rows > INT32_MAX - 1024 || d->batch > INT32_MAX) return MS_ERR_SHAPE;
     if (rows > 0) {
         const int64_t H = d->nheads, G = d->kv_heads;
         if (!offsets_ok(nb, d->q_sb, rows, d->q_sl, H, d->q_sh, d->dk) ||

@@ -18,17 +18,20 @@
 // it, never where it is kept.
 //
 // A CTA owns one (segment of a sequence, head, 64 columns of z) and walks its
-// chunks with the state in registers. One warp loads (tensor copies, 128-byte
-// swizzle, NS stages), one issues every product, and three groups of four warps
-// work on different chunks at the same time:
-//   group P  weights QK into P (tensor memory, in place), then adds up O_a and
-//            lam^.. O_b and writes o;
+// chunks with the state in registers. What bounds it is shared memory: a chunk
+// moves some 370 KB of it at dx = 128 (operands of the products 208, tensor
+// copies 80, Z' 64, S 16), 2900 clocks at 128 bytes a clock, so KV takes the three
+// parts of Z' as one product of N = 192 (24 products of N = 64 read Y three times,
+// and took 1900 clocks a chunk against 800). The roles run on different chunks at
+// the same time, each warp waiting for its own inputs only:
+//   one warp loads (tensor copies, 128-byte swizzle, NS stages); one warp each
+//   issues QK, KV, and O_a with O_b;
+//   group P  weights QK into P (tensor memory, in place);
+//   group E  adds up O_a and lam^.. O_b and writes o;
 //   group V  forms Z', and clears the rows of a chunk's Y and Z that are behind
 //            the sequence;
 //   group S  keeps S (a thread: one row, or half of one), adds KV, and hands
 //            its bf16 form to the next chunk's O_b.
-// The products of chunk c are issued as QK(c), KV(c), O_a(c-1), O_b(c), so the
-// tensor pipe works while groups P and S turn its results around.
 //
 // Where sequences times heads leave SMs idle, sequences are cut into segments:
 // a first pass (kStates) forms each segment's own state from zero, a second
@@ -38,6 +41,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -52,16 +56,15 @@ namespace {
 
 constexpr int kC = 128;   // tokens per chunk
 constexpr int kZ = 64;    // columns of z per CTA
-constexpr int kThreads = 448;
-constexpr int kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kThreads = 640;
+constexpr int kLoadWarp = 16, kQkWarp = 17, kKvWarp = 18, kOWarp = 19;  // groups P, V, S, E: warps 0-3, 4-7, 8-11, 12-15
 constexpr uint32_t kSpinTries = 1u << 20;
 
 // tensor memory: two buffers of QK (P takes its first 64 columns, O_a its last
-// 64), of O_b and of KV
+// 64), O_b, and the three parts of KV
 __host__ __device__ constexpr uint32_t col_qk(int b) { return 128u * b; }
 __host__ __device__ constexpr uint32_t col_oa(int b) { return 128u * b + 64u; }
-__host__ __device__ constexpr uint32_t col_ob(int b) { return 256u + 64u * b; }
-__host__ __device__ constexpr uint32_t col_kv(int b) { return 384u + 64u * b; }
+constexpr uint32_t kColOb = 256, kColKv = 320;
 
 struct TcProblem {
     int mx, my, mz;  // tensor maps of x, y, z
@@ -79,9 +82,9 @@ struct TcArgs {
     const float *log_decay;
     const int32_t *seq_start;
     int *status;
-    int64_t batch, seqlen, total, H;
-    int64_t seg;   // tokens per segment (a multiple of kC)
-    int64_t nseg;  // segments per sequence (dense); slots of the packed case are numbered below
+    int batch, seqlen, total, H;
+    int seg;   // tokens per segment (a multiple of kC)
+    int nseg;  // segments per sequence (dense); slots of the packed case are numbered below
     int segmented;
     int np, units;  // units: sum of nzb
     TcProblem p[kLaMaxProblems];
@@ -101,24 +104,27 @@ struct Smem {
     static constexpr int oZs = kStages * kStage;             // three parts of Z'
     static constexpr int oS = oZs + 3 * kZb;                 // S in bf16
     static constexpr int oPw = oS + (kStates ? 0 : DX * kZ * 2);  // lam^n, n = 0..128
-    static constexpr int oPs = oPw + 132 * 4;                // ps lam^n
-    static constexpr int oBar = oPs + 132 * 4;
-    static constexpr int kBytes = oBar + 8 * 24 + 16;
+    static constexpr int oPs = oPw + (132 + 32) * 4;         // ps lam^n, behind 32 zeros
+    static constexpr int oCf = oPs + 132 * 4;                // lam^(31-c), in reverse lam^c, c < 32
+    static constexpr int oBar = oCf + 32 * 4;
+    static constexpr int kBytes = oBar + 8 * 26 + 16;
 };
 enum {
-    kBarFull = 0,             // [3] a stage's tiles are in
-    kBarFree = 3,             // [3] every product reading the stage is done
-    kBarQK = 6,               // [2] QK is done
-    kBarP = 8,                // [2] P is in tensor memory
-    kBarO = 10,               // [2] O_a and O_b are done
-    kBarOFree = 12,           // [2] group P has read them
-    kBarKV = 14,              // [2] KV is done (and Z' read)
-    kBarKVFree = 16,          // [2] group S has read it
-    kBarZs = 18,              // Z' is in shared memory
-    kBarS = 19,               // S is in shared memory
-    kBarOB = 20,              // O_b is done (and S read)
-    kBarEnd = 21,
-    kNumBars = 22
+    kBarFull = 0,    // [3] a stage's tiles are in
+    kBarFree = 3,    // [3] every product reading the stage is done
+    kBarQK = 6,      // [2] QK is done
+    kBarP = 8,       // [2] P is in tensor memory
+    kBarO = 10,      // [2] O_a and O_b are done
+    kBarOFree = 12,  // [2] group E has read O_a (and O_b)
+    kBarZs = 14,     // [2] Z' of 64 tokens is in shared memory
+    kBarZsFree = 16, // [2] KV has read it
+    kBarKV = 18,     // KV is done
+    kBarKVFree = 19, // group S has read it
+    kBarS = 20,      // S is in shared memory
+    kBarOB = 21,     // O_b is done (and S read)
+    kBarClear = 22,  // the rows behind the sequence are cleared (once, in the chunk that has some)
+    kBarEnd = 23,    // [3] nothing of an issuing warp is in flight
+    kNumBars = 26
 };
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -177,8 +183,10 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
         : "memory");
     return done != 0;
 }
-// Waits for phase `k` of a barrier; false when the CTA is stopping or the wait ran out.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t k, volatile uint32_t *abort_flag, int *status) {
+// Waits for phase `k` of a barrier; false when the CTA is stopping or the wait
+// ran out. Only the first try is inlined: the roles' loops have to share the
+// SM's instruction cache (see the kernel).
+__device__ __noinline__ bool bar_wait_on(uint32_t bar, uint32_t k, volatile uint32_t *abort_flag, int *status) {
     for (uint32_t i = 0; i < kSpinTries; ++i) {
         if (bar_try(bar, k & 1u)) return true;
         if ((i & 63u) == 63u && *abort_flag != 0u) return false;
@@ -186,6 +194,9 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t k, volatile uint
     *abort_flag = 1u;
     if (status) atomicOr(status, MS_ERR_TIMEOUT);
     return false;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t k, volatile uint32_t *abort_flag, int *status) {
+    return bar_try(bar, k & 1u) || bar_wait_on(bar, k, abort_flag, status);
 }
 __device__ __forceinline__ void tma_load4(const CUtensorMap *map, uint32_t dst, uint32_t bar, int c0, int c1, int c2,
                                           int c3) {
@@ -209,6 +220,26 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
         : "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// 16 columns from each of two places, and 8 from each of three, waited for in the same statement
+__device__ __forceinline__ void tmem_ld2x16(uint32_t ta, uint32_t tb, float (&a)[16], float (&b)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]), "=f"(a[8]), "=f"(a[9]), "=f"(a[10]), "=f"(a[11]), "=f"(a[12]), "=f"(a[13]), "=f"(a[14]), "=f"(a[15]), "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]), "=f"(b[6]), "=f"(b[7]), "=f"(b[8]), "=f"(b[9]), "=f"(b[10]), "=f"(b[11]), "=f"(b[12]), "=f"(b[13]), "=f"(b[14]), "=f"(b[15])
+        : "r"(ta), "r"(tb)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld3x8(uint32_t ta, uint32_t tb, uint32_t tc, float (&a)[8], float (&b)[8], float (&c)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%24];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%25];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%16, %17, %18, %19, %20, %21, %22, %23}, [%26];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(a[0]), "=f"(a[1]), "=f"(a[2]), "=f"(a[3]), "=f"(a[4]), "=f"(a[5]), "=f"(a[6]), "=f"(a[7]), "=f"(b[0]), "=f"(b[1]), "=f"(b[2]), "=f"(b[3]), "=f"(b[4]), "=f"(b[5]), "=f"(b[6]), "=f"(b[7]), "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]), "=f"(c[4]), "=f"(c[5]), "=f"(c[6]), "=f"(c[7])
+        : "r"(ta), "r"(tb), "r"(tc)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -240,38 +271,38 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t 
 // segment; packed, floor(first row / seg) + sequence + segment, which gives each
 // sequence as many numbers as it has segments or more. Every lane returns the same.
 struct Place {
-    int64_t seq, g, row0, len, ng;
+    int seq, g, row0, len, ng;
     bool ok, bad;  // a segment of the sequence; offsets out of order
 };
-__device__ __forceinline__ Place place_of(const TcArgs &a, int64_t slot, int lane) {
+__device__ __forceinline__ Place place_of(const TcArgs &a, int slot, int lane) {
     Place p{};
+    int64_t len = a.seqlen;
     if (a.seq_start == nullptr) {
         p.seq = slot / a.nseg;
         p.g = slot % a.nseg;
-        p.len = a.seqlen;
     } else {
-        int64_t base = slot;
         p.seq = slot;
         if (a.segmented) {
             // the last sequence whose first slot is not behind this one
+            int base = 0;
             p.seq = 0;
-            base = 0;
-            for (int64_t i0 = 0; i0 < a.batch; i0 += 32) {
-                const int64_t i = i0 + lane;
-                const int64_t bi = i < a.batch ? a.seq_start[i] / a.seg + i : INT64_MAX;
+            for (int i0 = 0; i0 < a.batch; i0 += 32) {
+                const int i = i0 + lane;
+                const int bi = i < a.batch ? a.seq_start[i] / a.seg + i : INT_MAX;
                 const unsigned m = __ballot_sync(0xffffffffu, bi <= slot);
                 if (m == 0u) break;
                 const int last = 31 - __clz(m);
                 p.seq = i0 + last;
                 base = __shfl_sync(0xffffffffu, bi, last);
             }
+            p.g = slot - base;
         }
         const int64_t s = a.seq_start[p.seq], e = a.seq_start[p.seq + 1];
-        p.g = slot - base;
-        p.row0 = s;
-        p.len = e - s;
+        p.row0 = (int)s;
+        len = e - s;
         p.bad = !(s >= 0 && e >= s && e <= a.total);
     }
+    p.len = p.bad ? 0 : (int)len;
     p.ng = p.len > a.seg ? (p.len + a.seg - 1) / a.seg : 1;
     p.ok = !p.bad && p.g >= 0 && p.g < p.ng;
     return p;
@@ -286,12 +317,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = saddr(smem);
     auto bar = [&](int i) { return sbase + (uint32_t)(M::oBar + 8 * i); };
-    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * 24);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * 26);
     volatile uint32_t *abort_flag = misc + 1;
     float *pw = reinterpret_cast<float *>(smem + M::oPw), *pwp = reinterpret_cast<float *>(smem + M::oPs);
+    float *cfw = reinterpret_cast<float *>(smem + M::oCf);
 
     int unit = (int)(blockIdx.x % (unsigned)a.units);
-    const int64_t hs = blockIdx.x / (unsigned)a.units, h = hs % a.H, slot = hs / a.H;
+    const int hs = (int)(blockIdx.x / (unsigned)a.units), h = hs % a.H, slot = hs / a.H;
     int pi = 0;
     while (unit >= a.p[pi].nzb) unit -= a.p[pi++].nzb;
     const TcProblem &p = a.p[pi];
@@ -299,15 +331,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     const Place pl = place_of(a, slot, lane);
     if (pl.bad && tid == 0 && a.status) atomicOr(a.status, MS_ERR_SHAPE);
     if (!pl.ok || (kStates && (p.rev ? pl.g == 0 : pl.g == pl.ng - 1))) return;
-    const int64_t seg0 = pl.g * a.seg;
-    const int64_t ntok = pl.len - seg0 < a.seg ? pl.len - seg0 : a.seg;
-    const int nc = (int)((ntok + kC - 1) / kC);
+    const int seg0 = pl.g * a.seg;
+    const int ntok = pl.len - seg0 < a.seg ? pl.len - seg0 : a.seg;
+    const int nc = (ntok + kC - 1) / kC;
     const bool rev = p.rev != 0;
     // chunk c in the order of work: its first token, and how many it has
-    auto first_of = [&](int c) { return seg0 + (int64_t)(rev ? nc - 1 - c : c) * kC; };
+    auto first_of = [&](int c) { return seg0 + (rev ? nc - 1 - c : c) * kC; };
     auto count_of = [&](int c) {
-        const int64_t left = ntok - (int64_t)(rev ? nc - 1 - c : c) * kC;
-        return (int)(left < kC ? left : kC);
+        const int left = ntok - (rev ? nc - 1 - c : c) * kC;
+        return left < kC ? left : kC;
     };
 
     const float g = fmaxf(__ldg(a.log_decay + h), -1e30f);  // -inf: 0 * -inf must be 0
@@ -315,17 +347,20 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         const float w = expf((float)tid * g);
         pw[tid] = w;
         pwp[tid] = p.ps * w;
+        if (tid < 32) pwp[tid - 32] = 0.0f;
+        if (tid < 32) cfw[p.rev ? tid : 31 - tid] = w;
     }
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             const bool warps4 = (i >= kBarP && i < kBarP + 2) || (i >= kBarOFree && i < kBarOFree + 2) ||
-                                (i >= kBarKVFree && i < kBarKVFree + 2) || i == kBarZs || i == kBarS;
-            bar_init(bar(i), warps4 ? 4 : 1);
+                                (i >= kBarZs && i < kBarZs + 2) || i == kBarKVFree || i == kBarS || i == kBarClear;
+            const bool stage = i >= kBarFree && i < kBarFree + 3;  // QK, KV, O: each commits once
+            bar_init(bar(i), warps4 ? 4 : (stage && !kStates) ? 3 : 1);
         }
         misc[1] = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kMmaWarp) {
+    if (warp == kQkWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(misc)), "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -337,6 +372,12 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     auto wait = [&](int i, int k) { return bar_wait(bar(i), (uint32_t)k, abort_flag, a.status); };
     auto wait_all = [&](int i, int k) { return __all_sync(0xffffffffu, wait(i, k)) != 0; };  // whole warps: one answer
 
+    // every product that an issuing thread has in flight completes before the tensor memory is freed
+    auto drain = [&](int i) {
+        mma_commit(bar(kBarEnd + i));
+        for (uint32_t k = 0; k < kSpinTries && !bar_try(bar(kBarEnd + i), 0u); ++k) {}
+    };
+
     if (warp == kLoadWarp) {
         if (lane == 0) {
             const CUtensorMap *mx = &maps.m[p.mx], *my = &maps.m[p.my], *mz = &maps.m[p.mz];
@@ -347,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 const int st = c % NS;
                 if (c >= NS && !wait(kBarFree + st, c / NS - 1)) break;
                 const uint32_t dst = sbase + (uint32_t)(st * M::kStage), br = bar(kBarFull + st);
-                const int t = (int)(pl.row0 + first_of(c));
+                const int t = pl.row0 + first_of(c);
                 bar_arrive_tx(br, (uint32_t)M::kStage);
 #pragma unroll
                 for (int i = 0; i < DX / 64; ++i) tma_load4(my, dst + M::kX + i * 16384, br, 64 * i, hy, t, b);
@@ -362,124 +403,86 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 for (int i = c > NS ? c - NS : 0; i < c; ++i)
                     for (uint32_t k = 0; k < kSpinTries && !bar_try(bar(kBarFull + i % NS), (uint32_t)(i / NS) & 1u); ++k) {}
         }
-    } else if (warp == kMmaWarp) {
-        if (lane == 0) {
-            const int ksteps = (p.dx + 15) >> 4;
-            bool ok = true;
-            auto tiles = [&](int c) { return sbase + (uint32_t)((c % NS) * M::kStage); };
-            auto issue_oa = [&](int c) {
-                const uint32_t z = tiles(c) + M::kX + M::kY;
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_ts(tmem + col_oa(c & 1), tmem + col_qk(c & 1) + 8u * k, sdesc(z + 2048 * k, 0),
-                           idesc(kZ, false, true), k > 0);
-                mma_commit(bar(kBarO + (c & 1)));
-                mma_commit(bar(kBarFree + c % NS));
-            };
-            for (int c = 0; c < nc && ok; ++c) {
-                const int b = c & 1, st = c % NS;
-                const uint32_t x = tiles(c), y = x + M::kX;
-                if (!(ok = wait(kBarFull + st, c / NS))) break;
-                if constexpr (!kStates) {
-                    if (c >= 2 && !(ok = wait(kBarOFree + b, (c - 2) >> 1))) break;
+    } else if (warp == kQkWarp) {
+        if constexpr (!kStates) {
+            if (lane == 0) {
+                const int ksteps = (p.dx + 15) >> 4;
+                for (int c = 0; c < nc; ++c) {
+                    const int b = c & 1, st = c % NS;
+                    const uint32_t x = sbase + (uint32_t)(st * M::kStage), y = x + M::kX;
+                    if (!wait(kBarFull + st, c / NS) || (count_of(c) < kC && !wait(kBarClear, 0)) ||
+                        (c >= 2 && !wait(kBarOFree + b, (c - 2) >> 1)))
+                        break;
                     tc_after();
+#pragma unroll 1
                     for (int k = 0; k < ksteps; ++k) {
                         const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
                         mma(tmem + col_qk(b), sdesc(x + off, 0), sdesc(y + off, 0), idesc(kC, false, false), k > 0);
                     }
                     mma_commit(bar(kBarQK + b));
-                }
-                if (!(ok = wait(kBarZs, c))) break;
-                if (c >= 2 && !(ok = wait(kBarKVFree + b, (c - 2) >> 1))) break;
-                tc_after();
-#pragma unroll
-                for (int part = 0; part < 3; ++part)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        // dx <= 64: the second 64 rows of the product repeat the first
-                        mma(tmem + col_kv(b), sdesc(y + 2048 * k, DX == 64 ? 0 : 16384),
-                            sdesc(sbase + M::oZs + part * M::kZb + 2048 * k, 0), idesc(kZ, true, true), part > 0 || k > 0);
-                mma_commit(bar(kBarKV + b));
-                if constexpr (kStates) {
                     mma_commit(bar(kBarFree + st));
-                } else {
-                    if (c > 0) {
-                        if (!(ok = wait(kBarP + (b ^ 1), (c - 1) >> 1))) break;
-                        tc_after();
-                        issue_oa(c - 1);
-                    }
-                    if (!(ok = wait(kBarS, c))) break;
+                }
+                drain(0);
+            }
+        }
+    } else if (warp == kKvWarp) {
+        if (lane == 0) {
+            bool ok = true;
+            for (int c = 0; c < nc && ok; ++c) {
+                const int st = c % NS;
+                const uint32_t y = sbase + (uint32_t)(st * M::kStage + M::kX);
+                if (c > 0 && !(ok = wait(kBarKVFree, c - 1))) break;
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (!(ok = wait(kBarZs + hf, c))) break;
                     tc_after();
+#pragma unroll 1
+                    for (int k = 4 * hf; k < 4 * hf + 4; ++k)
+                        // dx <= 64: the second 64 rows of the product repeat the first
+                        mma(tmem + kColKv, sdesc(y + 2048 * k, DX == 64 ? 0 : 16384), sdesc(sbase + M::oZs + 2048 * k, M::kZb),
+                            idesc(3 * kZ, true, true), k > 0);
+                    mma_commit(bar(kBarZsFree + hf));
+                }
+                mma_commit(bar(kBarKV));
+                mma_commit(bar(kBarFree + st));
+            }
+            drain(1);
+        }
+    } else if (warp == kOWarp) {
+        if constexpr (!kStates) {
+            if (lane == 0) {
+                const int ksteps = (p.dx + 15) >> 4;
+                for (int c = 0; c < nc; ++c) {
+                    const int b = c & 1, st = c % NS;
+                    const uint32_t x = sbase + (uint32_t)(st * M::kStage), z = x + M::kX + M::kY;
+                    if (!wait(kBarFull + st, c / NS) || !wait(kBarS, c) || (c > 0 && !wait(kBarOFree + (b ^ 1), (c - 1) >> 1))) break;
+                    tc_after();
+#pragma unroll 1
                     for (int k = 0; k < ksteps; ++k)
-                        mma(tmem + col_ob(b), sdesc(x + (k >> 2) * 16384 + (k & 3) * 32, 0),
-                            sdesc(sbase + M::oS + 2048 * k, 0), idesc(kZ, false, true), k > 0);
+                        mma(tmem + kColOb, sdesc(x + (k >> 2) * 16384 + (k & 3) * 32, 0), sdesc(sbase + M::oS + 2048 * k, 0),
+                            idesc(kZ, false, true), k > 0);
                     mma_commit(bar(kBarOB));
-                }
-            }
-            if constexpr (!kStates) {
-                if (ok && nc > 0 && wait(kBarP + ((nc - 1) & 1), (nc - 1) >> 1)) {
+                    if (!wait(kBarP + b, c >> 1)) break;
                     tc_after();
-                    issue_oa(nc - 1);
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(tmem + col_oa(b), tmem + col_qk(b) + 8u * k, sdesc(z + 2048 * k, 0), idesc(kZ, false, true), k > 0);
+                    mma_commit(bar(kBarO + b));
+                    mma_commit(bar(kBarFree + st));
                 }
+                drain(2);
             }
-            // every product issued has completed before the tensor memory is freed
-            mma_commit(bar(kBarEnd));
-            for (uint32_t k = 0; k < kSpinTries && !bar_try(bar(kBarEnd), 0u); ++k) {}
         }
     } else if (warp < 4) {
         // ================================= group P =================================
         if constexpr (!kStates) {
             const int t = 32 * warp + lane;
             const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-            float cf[32];  // lam^(31-c), in reverse lam^c: a column's part of a full block's weights
-#pragma unroll
-            for (int i = 0; i < 32; ++i) cf[i] = pw[rev ? i : 31 - i];
-            const int64_t ob = (a.seq_start ? 0 : pl.seq * p.o_sb) + h * p.o_sh + kZ * zb;
-            const int cols = p.dz - kZ * zb < kZ ? p.dz - kZ * zb : kZ;
-            auto write_out = [&](int c) {
-                const int b = c & 1, n = count_of(c);
-                if (!wait_all(kBarO + b, c >> 1)) return false;
-                tc_after();
-                const float rf = t < n ? p.ro * pw[rev ? n - 1 - t : t + 1] : 0.0f;
-                const int64_t at = ob + (pl.row0 + first_of(c) + t) * p.o_sl;
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float oa[32], obv[32];
-                    tmem_ld32(lanes + col_oa(b) + 32u * hf, oa);
-                    tmem_ld32(lanes + col_ob(b) + 32u * hf, obv);
-                    if (hf == 1) {
-                        tc_before();
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(bar(kBarOFree + b));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) oa[i] = fmaf(rf, obv[i], oa[i]);
-                    if (t < n) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            const int col = 32 * hf + i;
-                            if (col < cols) {
-                                if (p.o_f32) {
-                                    float4 *o4 = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at + col);
-                                    o4[0] = make_float4(oa[i], oa[i + 1], oa[i + 2], oa[i + 3]);
-                                    o4[1] = make_float4(oa[i + 4], oa[i + 5], oa[i + 6], oa[i + 7]);
-                                } else {
-                                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + at + col) =
-                                        make_uint4(pack2(oa[i], oa[i + 1]), pack2(oa[i + 2], oa[i + 3]),
-                                                   pack2(oa[i + 4], oa[i + 5]), pack2(oa[i + 6], oa[i + 7]));
-                                }
-                            }
-                        }
-                    }
-                }
-                return true;
-            };
-            bool ok = true;
             for (int c = 0; c < nc; ++c) {
-                const int b = c & 1, n = count_of(c);
-                if (!(ok = wait_all(kBarQK + b, c >> 1))) break;
+                const uint32_t qk = lanes + col_qk(c & 1);
+                if (!wait_all(kBarQK + (c & 1), c >> 1)) break;
                 tc_after();
-#pragma unroll
+#pragma unroll 1
                 for (int jb = 0; jb < 4; ++jb) {
                     uint32_t r[16];
                     const int past = rev ? jb - warp : warp - jb;  // blocks between this one and the diagonal
@@ -488,73 +491,123 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                         for (int i = 0; i < 16; ++i) r[i] = 0u;
                     } else {
                         float v[32];
-                        tmem_ld32(lanes + col_qk(b) + 32u * jb, v);
+                        tmem_ld32(qk + 32u * jb, v);
+                        // lam^|t - s| from the row's distance to the block's edge and the column's; in
+                        // the block on the diagonal from the table, whose other side is zeros
                         if (past > 0) {
-                            const float rf = pwp[rev ? 32 * jb - t : t - 32 * jb - 31];
+                            const f2 rf = f2_splat(pwp[rev ? 32 * jb - t : t - 32 * jb - 31]);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] *= rf * cf[i];
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int d = rev ? i - lane : lane - i;
-                                v[i] = d >= 0 ? v[i] * pwp[d < 0 ? 0 : d] : 0.0f;
+                            for (int i = 0; i < 32; i += 4) {
+                                f2 w0, w1;
+                                lds_f2x2(cfw + i, w0, w1);
+                                f2_split(f2_mul(f2_make(v[i], v[i + 1]), f2_mul(rf, w0)), v[i], v[i + 1]);
+                                f2_split(f2_mul(f2_make(v[i + 2], v[i + 3]), f2_mul(rf, w1)), v[i + 2], v[i + 3]);
                             }
-                        }
-                        if (rev && n < kC) {
-                            // tokens behind the sequence come before these in this order
+                        } else {
+                            const float *w = pwp + (rev ? -lane : lane);
+                            if (rev) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (32 * jb + i >= n) v[i] = 0.0f;
+                                for (int i = 0; i < 32; ++i) v[i] *= w[i];
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) v[i] *= w[-i];
+                            }
                         }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) r[i] = pack2(v[2 * i], v[2 * i + 1]);
                     }
-                    tmem_st16(lanes + col_qk(b) + 16u * jb, r);
+                    tmem_st16(qk + 16u * jb, r);
                 }
                 tmem_st_wait();
                 tc_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(kBarP + b));
-                if (c > 0 && !(ok = write_out(c - 1))) break;
+                if (lane == 0) bar_arrive(bar(kBarP + (c & 1)));
             }
-            if (ok && nc > 0) write_out(nc - 1);
+        }
+    } else if (warp >= 12 && warp < 16) {
+        // ================================= group E =================================
+        if constexpr (!kStates) {
+            const int t = 32 * (warp - 12) + lane;
+            const uint32_t lanes = tmem + ((uint32_t)(32 * (warp - 12)) << 16);
+            const int64_t o0 = (a.seq_start ? 0 : (int64_t)pl.seq * p.o_sb) + (int64_t)h * p.o_sh + kZ * zb;
+            const int cols = p.dz - kZ * zb < kZ ? p.dz - kZ * zb : kZ;
+            for (int c = 0; c < nc; ++c) {
+                const int b = c & 1, n = count_of(c);
+                const float rf = t < n ? p.ro * pw[rev ? n - 1 - t : t + 1] : 0.0f;
+                const int64_t at = o0 + (int64_t)(pl.row0 + first_of(c) + t) * p.o_sl;
+                if (!wait_all(kBarO + b, c >> 1)) break;
+                tc_after();
+#pragma unroll 1
+                for (int i = 0; i < kZ; i += 16) {
+                    float v[16], ob[16];
+                    tmem_ld2x16(lanes + col_oa(b) + (uint32_t)i, lanes + kColOb + (uint32_t)i, v, ob);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = fmaf(rf, ob[j], v[j]);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 8)
+                        if (t < n && i + j < cols) {
+                            if (p.o_f32) {
+                                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at + i + j);
+                                o[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                                o[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
+                            } else {
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + at + i + j) =
+                                    make_uint4(pack2(v[j], v[j + 1]), pack2(v[j + 2], v[j + 3]), pack2(v[j + 4], v[j + 5]),
+                                               pack2(v[j + 6], v[j + 7]));
+                            }
+                        }
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(kBarOFree + b));
+            }
         }
     } else if (warp < 8) {
         // ================================= group V =================================
         const int gt = tid - 128;
-        for (int c = 0; c < nc; ++c) {
+        bool ok = true;
+        for (int c = 0; c < nc && ok; ++c) {
             const int st = c % NS, n = count_of(c);
             if (!wait_all(kBarFull + st, c / NS)) break;
-            if (c > 0 && !wait_all(kBarKV + ((c - 1) & 1), (c - 1) >> 1)) break;
             unsigned char *y = smem + st * M::kStage + M::kX, *z = y + M::kY, *zs = smem + M::oZs;
-#pragma unroll 2
-            for (int it = 0; it < 8; ++it) {
-                const int i = it * 128 + gt, row = i >> 3;
-                uint4 hi = make_uint4(0, 0, 0, 0), mid = hi, lo = hi;
-                if (row < n) {
-                    const float w = p.ws * pw[rev ? row + 1 : n - 1 - row];
-                    const uint4 q = *reinterpret_cast<const uint4 *>(z + 16 * i);
+            if (n < kC) {
+                // the rows behind the sequence, before any product reads them
+#pragma unroll 1
+                for (int i = n * 8 + gt; i < kC * 8; i += 128) {
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(z + 16 * i) = zero;
+#pragma unroll
+                    for (int j = 0; j < DX / 64; ++j) *reinterpret_cast<uint4 *>(y + j * 16384 + 16 * i) = zero;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(kBarClear));
+            }
+#pragma unroll 1
+            for (int hf = 0; hf < 2; ++hf) {
+                if (c > 0 && !(ok = wait_all(kBarZsFree + hf, c - 1))) break;
+#pragma unroll 1
+                for (int it = 0; it < 4; ++it) {
+                    const int i = hf * 512 + it * 128 + gt, row = i >> 3;
+                    uint4 hi, mid, lo;
+                    float w = 0.0f;
+                    uint4 q = make_uint4(0, 0, 0, 0);
+                    if (row < n) {
+                        w = p.ws * pw[rev ? row + 1 : n - 1 - row];
+                        q = *reinterpret_cast<const uint4 *>(z + 16 * i);
+                    }
                     split3(w * bf16_lo(q.x), w * bf16_hi(q.x), hi.x, mid.x, lo.x);
                     split3(w * bf16_lo(q.y), w * bf16_hi(q.y), hi.y, mid.y, lo.y);
                     split3(w * bf16_lo(q.z), w * bf16_hi(q.z), hi.z, mid.z, lo.z);
                     split3(w * bf16_lo(q.w), w * bf16_hi(q.w), hi.w, mid.w, lo.w);
-                } else {
-                    *reinterpret_cast<uint4 *>(z + 16 * i) = hi;
+                    *reinterpret_cast<uint4 *>(zs + 16 * i) = hi;
+                    *reinterpret_cast<uint4 *>(zs + M::kZb + 16 * i) = mid;
+                    *reinterpret_cast<uint4 *>(zs + 2 * M::kZb + 16 * i) = lo;
                 }
-                *reinterpret_cast<uint4 *>(zs + 16 * i) = hi;
-                *reinterpret_cast<uint4 *>(zs + M::kZb + 16 * i) = mid;
-                *reinterpret_cast<uint4 *>(zs + 2 * M::kZb + 16 * i) = lo;
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bar(kBarZs + hf));
             }
-            if (n < kC) {
-                // QK may be reading these rows of Y: they only reach scores that are not used
-                for (int i = n * 8 + gt; i < kC * 8; i += 128)
-#pragma unroll
-                    for (int hf = 0; hf < DX / 64; ++hf)
-                        *reinterpret_cast<uint4 *>(y + hf * 16384 + 16 * i) = make_uint4(0, 0, 0, 0);
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(kBarZs));
         }
     } else if (warp < 12) {
         // ================================= group S =================================
@@ -566,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         float S[NCOL];
         const int64_t blk = p.dx * (int64_t)p.dz;
         {
-            const float *s0 = p.s0 ? p.s0 + ((p.s0_slot ? slot : pl.seq) * a.H + h) * blk : nullptr;
+            const float *s0 = p.s0 ? p.s0 + ((int64_t)(p.s0_slot ? slot : pl.seq) * a.H + h) * blk : nullptr;
 #pragma unroll
             for (int i = 0; i < NCOL; ++i) {
                 const int col = kZ * zb + c0 + i;
@@ -574,8 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             }
         }
         bool ok = true;
+        const float m128 = expm1f((float)kC * g);
         for (int c = 0; c < nc; ++c) {
-            const int b = c & 1;
             if constexpr (!kStates) {
                 if (c > 0 && !(ok = wait_all(kBarOB, c - 1))) break;
                 unsigned char *dst = smem + M::oS + row * 128;
@@ -588,26 +641,28 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(kBarS));
             }
-            if (!(ok = wait_all(kBarKV + b, c >> 1))) break;
+            if (!(ok = wait_all(kBarKV, c))) break;
             tc_after();
             // lam^n S + KV as keep S + (part S + KV): with lam^n >= 1/2 part = lam^n - 1 keeps
             // the bits of a slow decay over many chunks
-            const float m = expm1f((float)count_of(c) * g);
+            const float m = count_of(c) == kC ? m128 : expm1f((float)count_of(c) * g);
             const float keep = m >= -0.5f ? 1.0f : 0.0f, part = m >= -0.5f ? m : pw[count_of(c)];
 #pragma unroll
-            for (int hf = 0; hf < NCOL / 32; ++hf) {
-                float kv[32];
-                tmem_ld32(lanes + col_kv(b) + (uint32_t)(c0 + 32 * hf), kv);
+            for (int i = 0; i < NCOL; i += 8) {
+                float hi[8], mid[8], lo[8];
+                const uint32_t at = lanes + kColKv + (uint32_t)(c0 + i);
+                tmem_ld3x8(at, at + kZ, at + 2 * kZ, hi, mid, lo);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) S[32 * hf + i] = fmaf(keep, S[32 * hf + i], fmaf(part, S[32 * hf + i], kv[i]));
+                for (int j = 0; j < 8; ++j)
+                    S[i + j] = fmaf(keep, S[i + j], fmaf(part, S[i + j], hi[j] + (mid[j] + lo[j])));
             }
             tc_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(bar(kBarKVFree + b));
+            if (lane == 0) bar_arrive(bar(kBarKVFree));
         }
         const bool last = rev ? pl.g == 0 : pl.g == pl.ng - 1;
         if (ok && p.fin && (kStates || last) && row < p.dx) {
-            float *f = p.fin + ((kStates ? slot : pl.seq) * a.H + h) * blk + row * (int64_t)p.dz + kZ * zb + c0;
+            float *f = p.fin + ((int64_t)(kStates ? slot : pl.seq) * a.H + h) * blk + row * (int64_t)p.dz + kZ * zb + c0;
 #pragma unroll
             for (int i = 0; i < NCOL; i += 4)
                 if (kZ * zb + c0 + i < p.dz) *reinterpret_cast<float4 *>(f + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
@@ -616,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
 
     tc_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kQkWarp) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
     }
@@ -632,7 +687,7 @@ struct ChainArgs {
 };
 __global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constant__ TcArgs a, const ChainArgs ch) {
     const int k = blockIdx.z;
-    const int64_t seq = blockIdx.y / a.H, h = blockIdx.y % a.H, blk = (int64_t)ch.dx[k] * ch.dz[k];
+    const int64_t seq = (int)blockIdx.y / a.H, h = (int)blockIdx.y % a.H, blk = (int64_t)ch.dx[k] * ch.dz[k];
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
     int64_t base = seq * a.nseg, len = a.seqlen;
     if (a.seq_start) {
@@ -735,7 +790,7 @@ cudaError_t launch_t(const TcArgs &a, const TcMaps &maps, int64_t slots, cudaStr
     cudaError_t e = opt_in.ensure(reinterpret_cast<const void *>(linattn_tc_kernel<DX, kStates>), bytes);
     if (e != cudaSuccess) return e;
     const int64_t grid = slots * a.H * a.units;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (grid > 0x7fffffffLL || a.seg <= 0) return cudaErrorInvalidConfiguration;
     linattn_tc_kernel<DX, kStates><<<(unsigned)grid, kThreads, bytes, stream>>>(a, maps);
     return cudaGetLastError();
 }
@@ -771,7 +826,7 @@ cudaError_t launch_linattn_tc(const LaArgs &la, void *workspace, int num_sms, cu
     a.log_decay = la.log_decay;
     a.seq_start = la.seq_start;
     a.status = la.status;
-    a.batch = la.batch; a.seqlen = la.seqlen; a.total = la.total; a.H = la.H;
+    a.batch = (int)la.batch; a.seqlen = (int)la.seqlen; a.total = (int)la.total; a.H = (int)la.H;
     a.np = la.np;
     TcMaps maps;
     MapKey keys[4];
@@ -799,8 +854,8 @@ cudaError_t launch_linattn_tc(const LaArgs &la, void *workspace, int num_sms, cu
         dxmax = std::max(dxmax, p.dx);
     }
     const SegPlan sp = seg_plan(la.batch, rows, packed, la.H, a.units, num_sms);
-    a.seg = sp.seg;
-    a.nseg = sp.nseg;
+    a.seg = (int)sp.seg;
+    a.nseg = (int)sp.nseg;
     a.segmented = sp.segmented ? 1 : 0;
     if (sp.segmented) {
         // the segments' own states: of the forward direction (problem 0), and of the reverse one
