@@ -56,8 +56,16 @@ namespace {
 
 constexpr int kC = 128;   // tokens per chunk
 constexpr int kZ = 64;    // columns of z per CTA
-constexpr int kThreads = 640;
-constexpr int kLoadWarp = 16, kQkWarp = 17, kKvWarp = 18, kOWarp = 19;  // groups P, V, S, E: warps 0-3, 4-7, 8-11, 12-15
+// The warps of a CTA: group P, group V, group S, group E, and one that loads and
+// three that issue. Group V sets the pace at dx <= 64, so there it has eight warps
+// (NNN); at dx = 128 the registers of S leave room for four.
+template <int DX>
+struct Roles {
+    static constexpr int kV = DX == 64 ? 8 : 4;
+    static constexpr int kV0 = 4, kS0 = kV0 + kV, kE0 = kS0 + 4;
+    static constexpr int kLoad = kE0 + 4, kQk = kLoad + 1, kKv = kLoad + 2, kO = kLoad + 3;
+    static constexpr int kThreads = 32 * (kO + 1);
+};
 constexpr uint32_t kSpinTries = 1u << 20;
 
 // tensor memory: two buffers of QK (P takes its first 64 columns, O_a its last
@@ -103,28 +111,34 @@ struct Smem {
     static constexpr int kStages = DX == 64 ? 3 : 2;
     static constexpr int oZs = kStages * kStage;             // three parts of Z'
     static constexpr int oS = oZs + 3 * kZb;                 // S in bf16
-    static constexpr int oPw = oS + (kStates ? 0 : DX * kZ * 2);  // lam^n, n = 0..128
-    static constexpr int oPs = oPw + (132 + 32) * 4;         // ps lam^n, behind 32 zeros
-    static constexpr int oCf = oPs + 132 * 4;                // lam^(31-c), in reverse lam^c, c < 32
+    static constexpr int oTv = oS + (kStates ? 0 : DX * kZ * 2);  // weights of Z's rows
+    static constexpr int oTe = oTv + 128 * 4;                // of O_b's rows
+    static constexpr int oPs = oTe + 128 * 4;                // ps lam^n
+    static constexpr int oDiag = oPs + 128 * 4;              // ps lam^|d| at 31 + d, d = t - s, 0 on the masked side
+    static constexpr int oCf = oDiag + 64 * 4;               // lam^(31-c), in reverse lam^c, c < 32
     static constexpr int oBar = oCf + 32 * 4;
-    static constexpr int kBytes = oBar + 8 * 26 + 16;
+    static constexpr int kBytes = oBar + 8 * 38 + 16;
 };
 enum {
-    kBarFull = 0,    // [3] a stage's tiles are in
-    kBarFree = 3,    // [3] every product reading the stage is done
-    kBarQK = 6,      // [2] QK is done
-    kBarP = 8,       // [2] P is in tensor memory
-    kBarO = 10,      // [2] O_a and O_b are done
-    kBarOFree = 12,  // [2] group E has read O_a (and O_b)
-    kBarZs = 14,     // [2] Z' of 64 tokens is in shared memory
-    kBarZsFree = 16, // [2] KV has read it
-    kBarKV = 18,     // KV is done
-    kBarKVFree = 19, // group S has read it
-    kBarS = 20,      // S is in shared memory
-    kBarOB = 21,     // O_b is done (and S read)
-    kBarClear = 22,  // the rows behind the sequence are cleared (once, in the chunk that has some)
-    kBarEnd = 23,    // [3] nothing of an issuing warp is in flight
-    kNumBars = 26
+    kBarX = 0,        // [3] a stage's X, Y, Z tiles are in
+    kBarY = 3,
+    kBarZ = 6,
+    kBarXFree = 9,    // [3] what uses the stage's X (QK, O_b), Y (QK, KV), Z (groups V, E) is done
+    kBarYFree = 12,
+    kBarZFree = 15,
+    kBarQK = 18,      // [2] QK is done
+    kBarP = 20,       // [2] P is in tensor memory
+    kBarO = 22,       // [2] O_a and O_b are done
+    kBarOFree = 24,   // [2] group E has read O_a (and O_b)
+    kBarZs = 26,      // [2] Z' of 64 tokens is in shared memory
+    kBarZsFree = 28,  // [2] KV has read it
+    kBarKV = 30,      // KV is done
+    kBarKVFree = 31,  // group S has read it
+    kBarS = 32,       // S is in shared memory
+    kBarOB = 33,      // O_b is done (and S read)
+    kBarClear = 34,   // the rows behind the sequence are cleared (once, in the chunk that has some)
+    kBarEnd = 35,     // [3] nothing of an issuing warp is in flight
+    kNumBars = 38
 };
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -137,6 +151,7 @@ __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lead) {
     return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
 }
+__device__ __forceinline__ uint64_t dstep(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }  // (no carry out of the address)
 // kind::f16, fp32 accumulator, bf16 operands, M = 128
 constexpr uint32_t idesc(int n, bool a_mn, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
@@ -185,7 +200,8 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
 }
 // Waits for phase `k` of a barrier; false when the CTA is stopping or the wait
 // ran out. Only the first try is inlined: the roles' loops have to share the
-// SM's instruction cache (see the kernel).
+// SM's instruction cache (see the kernel). (A warp's lanes all ask: one lane that
+// asks for the others took 8 % more of the whole.)
 __device__ __noinline__ bool bar_wait_on(uint32_t bar, uint32_t k, volatile uint32_t *abort_flag, int *status) {
     for (uint32_t i = 0; i < kSpinTries; ++i) {
         if (bar_try(bar, k & 1u)) return true;
@@ -250,6 +266,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+__device__ __forceinline__ void sts128(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -258,13 +282,19 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
-// v = hi + mid + lo in bf16 parts (24 significant bits), a pair at a time
-__device__ __forceinline__ void split3(float a, float b, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    hi = pack2(a, b);
-    a -= bf16_lo(hi);
-    b -= bf16_hi(hi);
-    mid = pack2(a, b);
-    lo = pack2(a - bf16_lo(mid), b - bf16_hi(mid));
+__device__ __forceinline__ uint32_t pack2(f2 v) {
+    float a, b;
+    f2_split(v, a, b);
+    return pack2(a, b);
+}
+__device__ __forceinline__ f2 unpack2(uint32_t v) { return f2_make(bf16_lo(v), bf16_hi(v)); }
+// w q = hi + mid + lo in bf16 parts (24 significant bits) for a pair q of bf16
+__device__ __forceinline__ void split3(f2 w, uint32_t q, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
+    f2 v = f2_mul(w, unpack2(q));
+    hi = pack2(v);
+    v = f2_sub(v, unpack2(hi));
+    mid = pack2(v);
+    lo = pack2(f2_sub(v, unpack2(mid)));
 }
 
 // The sequence and segment of a slot. Slot numbers: dense, sequence * nseg +
@@ -308,19 +338,22 @@ __device__ __forceinline__ Place place_of(const TcArgs &a, int slot, int lane) {
     return p;
 }
 
+// The roles' code is what the SM's instruction cache has to hold at once (five
+// groups of warps, each in a loop of its own): with the loops unrolled and the
+// call's parameters read inside them, warps waited for instructions half of the
+// time. So what a chunk needs is laid out before the loops (tables, addresses,
+// steps), and the loops are short.
 template <int DX, bool kStates>
-__global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcArgs a,
+__global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcArgs a,
                                                                  const __grid_constant__ TcMaps maps) {
     using M = Smem<DX, kStates>;
-    constexpr int NS = M::kStages;
+    using R = Roles<DX>;
+    constexpr int NS = M::kStages, KX = DX / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = saddr(smem);
-    auto bar = [&](int i) { return sbase + (uint32_t)(M::oBar + 8 * i); };
-    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * 26);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * 38);
     volatile uint32_t *abort_flag = misc + 1;
-    float *pw = reinterpret_cast<float *>(smem + M::oPw), *pwp = reinterpret_cast<float *>(smem + M::oPs);
-    float *cfw = reinterpret_cast<float *>(smem + M::oCf);
 
     int unit = (int)(blockIdx.x % (unsigned)a.units);
     const int hs = (int)(blockIdx.x / (unsigned)a.units), h = hs % a.H, slot = hs / a.H;
@@ -330,37 +363,50 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     const int zb = unit;
     const Place pl = place_of(a, slot, lane);
     if (pl.bad && tid == 0 && a.status) atomicOr(a.status, MS_ERR_SHAPE);
-    if (!pl.ok || (kStates && (p.rev ? pl.g == 0 : pl.g == pl.ng - 1))) return;
+    const bool rev = p.rev != 0;
+    if (!pl.ok || (kStates && (rev ? pl.g == 0 : pl.g == pl.ng - 1))) return;
     const int seg0 = pl.g * a.seg;
     const int ntok = pl.len - seg0 < a.seg ? pl.len - seg0 : a.seg;
     const int nc = (ntok + kC - 1) / kC;
-    const bool rev = p.rev != 0;
-    // chunk c in the order of work: its first token, and how many it has
-    auto first_of = [&](int c) { return seg0 + (rev ? nc - 1 - c : c) * kC; };
-    auto count_of = [&](int c) {
-        const int left = ntok - (rev ? nc - 1 - c : c) * kC;
-        return left < kC ? left : kC;
-    };
+    // the chunk (in the order of work) that is not full, if one is not, and its tokens
+    const int npart = ntok % kC == 0 ? kC : ntok % kC, cpart = npart == kC ? -1 : rev ? 0 : nc - 1;
+    // the first row of chunk c is row0 + c * dt
+    const int dt = rev ? -kC : kC, row0 = pl.row0 + seg0 + (rev ? (nc - 1) * kC : 0);
 
     const float g = fmaxf(__ldg(a.log_decay + h), -1e30f);  // -inf: 0 * -inf must be 0
-    if (tid <= kC) {
-        const float w = expf((float)tid * g);
-        pw[tid] = w;
-        pwp[tid] = p.ps * w;
-        if (tid < 32) pwp[tid - 32] = 0.0f;
-        if (tid < 32) cfw[p.rev ? tid : 31 - tid] = w;
+    if (tid < kC) {
+        float *tv = reinterpret_cast<float *>(smem + M::oTv), *te = reinterpret_cast<float *>(smem + M::oTe);
+        float *ps = reinterpret_cast<float *>(smem + M::oPs), *dg = reinterpret_cast<float *>(smem + M::oDiag);
+        float *cf = reinterpret_cast<float *>(smem + M::oCf);
+        const float w = expf((float)tid * g), w1 = expf((float)(tid + 1) * g);
+        if (rev) {
+            tv[tid] = p.ws * w1;
+            te[kC - 1 - tid] = p.ro * w;
+        } else {
+            tv[kC - 1 - tid] = p.ws * w;
+            te[tid] = p.ro * w1;
+        }
+        ps[tid] = p.ps * w;
+        if (tid < 32) {
+            dg[31 + tid] = rev && tid > 0 ? 0.0f : p.ps * w;
+            if (tid > 0) dg[31 - tid] = rev ? p.ps * w : 0.0f;
+            cf[rev ? tid : 31 - tid] = w;
+        }
     }
+    const uint32_t bars = sbase + (uint32_t)M::oBar;
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
             const bool warps4 = (i >= kBarP && i < kBarP + 2) || (i >= kBarOFree && i < kBarOFree + 2) ||
-                                (i >= kBarZs && i < kBarZs + 2) || i == kBarKVFree || i == kBarS || i == kBarClear;
-            const bool stage = i >= kBarFree && i < kBarFree + 3;  // QK, KV, O: each commits once
-            bar_init(bar(i), warps4 ? 4 : (stage && !kStates) ? 3 : 1);
+                                i == kBarKVFree || i == kBarS;
+            const bool warpsv = (i >= kBarZs && i < kBarZs + 2) || i == kBarClear;
+            const bool two = (i >= kBarXFree && i < kBarYFree) || (i >= kBarYFree && i < kBarZFree && !kStates);
+            const bool zfree = i >= kBarZFree && i < kBarZFree + 3;  // the warps of V and E
+            bar_init(bars + 8 * i, warps4 ? 4 : warpsv ? R::kV : two ? 2 : zfree ? (kStates ? R::kV : R::kV + 4) : 1);
         }
         misc[1] = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kQkWarp) {
+    if (warp == R::kQk) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(misc)), "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -369,106 +415,130 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
     __syncthreads();
     tc_after();
     const uint32_t tmem = misc[0];
+    auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
     auto wait = [&](int i, int k) { return bar_wait(bar(i), (uint32_t)k, abort_flag, a.status); };
     auto wait_all = [&](int i, int k) { return __all_sync(0xffffffffu, wait(i, k)) != 0; };  // whole warps: one answer
-
     // every product that an issuing thread has in flight completes before the tensor memory is freed
     auto drain = [&](int i) {
         mma_commit(bar(kBarEnd + i));
         for (uint32_t k = 0; k < kSpinTries && !bar_try(bar(kBarEnd + i), 0u); ++k) {}
     };
+    // stages go round: st = c % NS, and use = c / NS counts the rounds
+    struct Ring {
+        int st = 0, use = 0;
+        __device__ __forceinline__ void next() {
+            if (++st == NS) st = 0, ++use;
+        }
+    } ring;
 
-    if (warp == kLoadWarp) {
+    if (warp == R::kLoad) {
         if (lane == 0) {
             const CUtensorMap *mx = &maps.m[p.mx], *my = &maps.m[p.my], *mz = &maps.m[p.mz];
-            const int b = a.seq_start ? 0 : (int)pl.seq;
-            const int hx = (int)(h / p.xg), hy = (int)(h / p.yg), hz = (int)(h / p.zg);
-            int c = 0;
-            for (; c < nc; ++c) {
-                const int st = c % NS;
-                if (c >= NS && !wait(kBarFree + st, c / NS - 1)) break;
-                const uint32_t dst = sbase + (uint32_t)(st * M::kStage), br = bar(kBarFull + st);
-                const int t = pl.row0 + first_of(c);
-                bar_arrive_tx(br, (uint32_t)M::kStage);
+            const int b = a.seq_start ? 0 : pl.seq;
+            const int hx = h / p.xg, hy = h / p.yg, hz = h / p.zg;
+            int c = 0, t = row0, sent_of_last = 0;  // sent_of_last: of the chunk at which the loop stopped
+            bool ok = true;
+#pragma unroll 1
+            for (; c < nc; ++c, t += dt, ring.next()) {
+                const int st = ring.st, use = ring.use;
+                const uint32_t dst = sbase + (uint32_t)(st * M::kStage);
+                sent_of_last = 0;
+                if (use > 0 && !(ok = wait(kBarYFree + st, use - 1))) break;
+                bar_arrive_tx(bar(kBarY + st), (uint32_t)M::kY);
 #pragma unroll
-                for (int i = 0; i < DX / 64; ++i) tma_load4(my, dst + M::kX + i * 16384, br, 64 * i, hy, t, b);
-                tma_load4(mz, dst + M::kX + M::kY, br, kZ * zb, hz, t, b);
+                for (int i = 0; i < DX / 64; ++i) tma_load4(my, dst + M::kX + i * 16384, bar(kBarY + st), 64 * i, hy, t, b);
+                sent_of_last = 1;
+                if (use > 0 && !(ok = wait(kBarZFree + st, use - 1))) break;
+                bar_arrive_tx(bar(kBarZ + st), (uint32_t)M::kZb);
+                tma_load4(mz, dst + M::kX + M::kY, bar(kBarZ + st), kZ * zb, hz, t, b);
+                sent_of_last = 2;
                 if constexpr (!kStates) {
+                    if (use > 0 && !(ok = wait(kBarXFree + st, use - 1))) break;
+                    bar_arrive_tx(bar(kBarX + st), (uint32_t)M::kX);
 #pragma unroll
-                    for (int i = 0; i < DX / 64; ++i) tma_load4(mx, dst + i * 16384, br, 64 * i, hx, t, b);
+                    for (int i = 0; i < DX / 64; ++i) tma_load4(mx, dst + i * 16384, bar(kBarX + st), 64 * i, hx, t, b);
                 }
             }
             // when stopping, the copies issued have landed before the CTA ends
-            if (c < nc)
-                for (int i = c > NS ? c - NS : 0; i < c; ++i)
-                    for (uint32_t k = 0; k < kSpinTries && !bar_try(bar(kBarFull + i % NS), (uint32_t)(i / NS) & 1u); ++k) {}
+            for (int q = 0; q < 3 && !ok; ++q) {
+                const int at = q == 0 ? kBarY : q == 1 ? kBarZ : kBarX, last = q < sent_of_last ? c : c - 1;
+                for (int i = last < NS ? 0 : last - NS + 1; i <= last && (q < 2 || !kStates); ++i)
+                    for (uint32_t k = 0; k < kSpinTries && !bar_try(bar(at + i % NS), (uint32_t)(i / NS) & 1u); ++k) {}
+            }
         }
-    } else if (warp == kQkWarp) {
+    } else if (warp == R::kQk) {
         if constexpr (!kStates) {
             if (lane == 0) {
-                const int ksteps = (p.dx + 15) >> 4;
-                for (int c = 0; c < nc; ++c) {
-                    const int b = c & 1, st = c % NS;
-                    const uint32_t x = sbase + (uint32_t)(st * M::kStage), y = x + M::kX;
-                    if (!wait(kBarFull + st, c / NS) || (count_of(c) < kC && !wait(kBarClear, 0)) ||
+                const uint64_t dx0 = sdesc(sbase, 0), dy0 = sdesc(sbase + M::kX, 0);
+#pragma unroll 1
+                for (int c = 0; c < nc; ++c, ring.next()) {
+                    const int b = c & 1, st = ring.st;
+                    if (!wait(kBarX + st, ring.use) || !wait(kBarY + st, ring.use) || (c == cpart && !wait(kBarClear, 0)) ||
                         (c >= 2 && !wait(kBarOFree + b, (c - 2) >> 1)))
                         break;
                     tc_after();
-#pragma unroll 1
-                    for (int k = 0; k < ksteps; ++k) {
+                    const uint64_t x = dstep(dx0, st * M::kStage), y = dstep(dy0, st * M::kStage);
+#pragma unroll
+                    for (int k = 0; k < KX; ++k) {
                         const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
-                        mma(tmem + col_qk(b), sdesc(x + off, 0), sdesc(y + off, 0), idesc(kC, false, false), k > 0);
+                        mma(tmem + col_qk(b), dstep(x, off), dstep(y, off), idesc(kC, false, false), k > 0);
                     }
                     mma_commit(bar(kBarQK + b));
-                    mma_commit(bar(kBarFree + st));
+                    mma_commit(bar(kBarXFree + st));
+                    mma_commit(bar(kBarYFree + st));
                 }
                 drain(0);
             }
         }
-    } else if (warp == kKvWarp) {
+    } else if (warp == R::kKv) {
         if (lane == 0) {
+            // dx <= 64: the second 64 rows of the product repeat the first
+            const uint64_t dy0 = sdesc(sbase + M::kX, DX == 64 ? 0 : 16384), dz = sdesc(sbase + M::oZs, M::kZb);
             bool ok = true;
-            for (int c = 0; c < nc && ok; ++c) {
-                const int st = c % NS;
-                const uint32_t y = sbase + (uint32_t)(st * M::kStage + M::kX);
-                if (c > 0 && !(ok = wait(kBarKVFree, c - 1))) break;
+#pragma unroll 1
+            for (int c = 0; c < nc && ok; ++c, ring.next()) {
+                const int st = ring.st;
+                const uint64_t y = dstep(dy0, st * M::kStage);
+                if (!(ok = wait(kBarY + st, ring.use)) || (c > 0 && !(ok = wait(kBarKVFree, c - 1)))) break;
 #pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf) {
                     if (!(ok = wait(kBarZs + hf, c))) break;
                     tc_after();
-#pragma unroll 1
-                    for (int k = 4 * hf; k < 4 * hf + 4; ++k)
-                        // dx <= 64: the second 64 rows of the product repeat the first
-                        mma(tmem + kColKv, sdesc(y + 2048 * k, DX == 64 ? 0 : 16384), sdesc(sbase + M::oZs + 2048 * k, M::kZb),
-                            idesc(3 * kZ, true, true), k > 0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma(tmem + kColKv, dstep(y, 8192 * hf + 2048 * k), dstep(dz, 8192 * hf + 2048 * k),
+                            idesc(3 * kZ, true, true), hf > 0 || k > 0);
                     mma_commit(bar(kBarZsFree + hf));
                 }
                 mma_commit(bar(kBarKV));
-                mma_commit(bar(kBarFree + st));
+                mma_commit(bar(kBarYFree + st));
             }
             drain(1);
         }
-    } else if (warp == kOWarp) {
+    } else if (warp == R::kO) {
         if constexpr (!kStates) {
             if (lane == 0) {
-                const int ksteps = (p.dx + 15) >> 4;
-                for (int c = 0; c < nc; ++c) {
-                    const int b = c & 1, st = c % NS;
-                    const uint32_t x = sbase + (uint32_t)(st * M::kStage), z = x + M::kX + M::kY;
-                    if (!wait(kBarFull + st, c / NS) || !wait(kBarS, c) || (c > 0 && !wait(kBarOFree + (b ^ 1), (c - 1) >> 1))) break;
-                    tc_after();
+                const uint64_t dx0 = sdesc(sbase, 0), dz0 = sdesc(sbase + M::kX + M::kY, 0), ds = sdesc(sbase + M::oS, 0);
 #pragma unroll 1
-                    for (int k = 0; k < ksteps; ++k)
-                        mma(tmem + kColOb, sdesc(x + (k >> 2) * 16384 + (k & 3) * 32, 0), sdesc(sbase + M::oS + 2048 * k, 0),
+                for (int c = 0; c < nc; ++c, ring.next()) {
+                    const int b = c & 1, st = ring.st;
+                    if (!wait(kBarX + st, ring.use) || !wait(kBarZ + st, ring.use) || !wait(kBarS, c) ||
+                        (c > 0 && !wait(kBarOFree + (b ^ 1), (c - 1) >> 1)))
+                        break;
+                    tc_after();
+                    const uint64_t x = dstep(dx0, st * M::kStage), z = dstep(dz0, st * M::kStage);
+#pragma unroll
+                    for (int k = 0; k < KX; ++k)
+                        mma(tmem + kColOb, dstep(x, (k >> 2) * 16384 + (k & 3) * 32), dstep(ds, 2048 * k),
                             idesc(kZ, false, true), k > 0);
                     mma_commit(bar(kBarOB));
+                    mma_commit(bar(kBarXFree + st));
                     if (!wait(kBarP + b, c >> 1)) break;
                     tc_after();
-#pragma unroll 1
+#pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_ts(tmem + col_oa(b), tmem + col_qk(b) + 8u * k, sdesc(z + 2048 * k, 0), idesc(kZ, false, true), k > 0);
+                        mma_ts(tmem + col_oa(b), tmem + col_qk(b) + 8u * k, dstep(z, 2048 * k), idesc(kZ, false, true), k > 0);
                     mma_commit(bar(kBarO + b));
-                    mma_commit(bar(kBarFree + st));
                 }
                 drain(2);
             }
@@ -478,43 +548,42 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
         if constexpr (!kStates) {
             const int t = 32 * warp + lane;
             const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
+            // a block of 32 columns before the diagonal: lam^|t - s| from the row's distance to the
+            // block's edge (rf, a step per block) and the column's (cf); the block on the diagonal
+            // from a table by t - s, one side of which is zeros; behind it, zeros
+            const float *cf = reinterpret_cast<const float *>(smem + M::oCf);
+            const float *dg = reinterpret_cast<const float *>(smem + M::oDiag) + 31 + lane;
+            const float *rf0 = reinterpret_cast<const float *>(smem + M::oPs) + (rev ? -t : t - 31);
+            const int past0 = rev ? -warp : warp, dpast = rev ? 1 : -1, drf = rev ? 32 : -32;
+#pragma unroll 1
             for (int c = 0; c < nc; ++c) {
                 const uint32_t qk = lanes + col_qk(c & 1);
                 if (!wait_all(kBarQK + (c & 1), c >> 1)) break;
                 tc_after();
+                int past = past0;  // blocks between this one and the diagonal
+                const float *rf = rf0;
 #pragma unroll 1
-                for (int jb = 0; jb < 4; ++jb) {
+                for (int jb = 0; jb < 4; ++jb, past += dpast, rf += drf) {
                     uint32_t r[16];
-                    const int past = rev ? jb - warp : warp - jb;  // blocks between this one and the diagonal
                     if (past < 0) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) r[i] = 0u;
                     } else {
                         float v[32];
                         tmem_ld32(qk + 32u * jb, v);
-                        // lam^|t - s| from the row's distance to the block's edge and the column's; in
-                        // the block on the diagonal from the table, whose other side is zeros
                         if (past > 0) {
-                            const f2 rf = f2_splat(pwp[rev ? 32 * jb - t : t - 32 * jb - 31]);
+                            const f2 w = f2_splat(*rf);
 #pragma unroll
                             for (int i = 0; i < 32; i += 4) {
                                 f2 w0, w1;
-                                lds_f2x2(cfw + i, w0, w1);
-                                f2_split(f2_mul(f2_make(v[i], v[i + 1]), f2_mul(rf, w0)), v[i], v[i + 1]);
-                                f2_split(f2_mul(f2_make(v[i + 2], v[i + 3]), f2_mul(rf, w1)), v[i + 2], v[i + 3]);
+                                lds_f2x2(cf + i, w0, w1);
+                                r[i / 2] = pack2(f2_mul(f2_make(v[i], v[i + 1]), f2_mul(w, w0)));
+                                r[i / 2 + 1] = pack2(f2_mul(f2_make(v[i + 2], v[i + 3]), f2_mul(w, w1)));
                             }
                         } else {
-                            const float *w = pwp + (rev ? -lane : lane);
-                            if (rev) {
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] *= w[i];
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] *= w[-i];
-                            }
+                            for (int i = 0; i < 32; i += 2) r[i / 2] = pack2(v[i] * dg[-i], v[i + 1] * dg[-i - 1]);
                         }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = pack2(v[2 * i], v[2 * i + 1]);
                     }
                     tmem_st16(qk + 16u * jb, r);
                 }
@@ -524,137 +593,194 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
                 if (lane == 0) bar_arrive(bar(kBarP + (c & 1)));
             }
         }
-    } else if (warp >= 12 && warp < 16) {
+    } else if (warp >= R::kE0) {
         // ================================= group E =================================
         if constexpr (!kStates) {
-            const int t = 32 * (warp - 12) + lane;
-            const uint32_t lanes = tmem + ((uint32_t)(32 * (warp - 12)) << 16);
-            const int64_t o0 = (a.seq_start ? 0 : (int64_t)pl.seq * p.o_sb) + (int64_t)h * p.o_sh + kZ * zb;
+            const int t = 32 * (warp - R::kE0) + lane;
+            const uint32_t lanes = tmem + ((uint32_t)(32 * (warp - R::kE0)) << 16);
             const int cols = p.dz - kZ * zb < kZ ? p.dz - kZ * zb : kZ;
-            for (int c = 0; c < nc; ++c) {
-                const int b = c & 1, n = count_of(c);
-                const float rf = t < n ? p.ro * pw[rev ? n - 1 - t : t + 1] : 0.0f;
-                const int64_t at = o0 + (int64_t)(pl.row0 + first_of(c) + t) * p.o_sl;
+            const int64_t at = (a.seq_start ? 0 : (int64_t)pl.seq * p.o_sb) + (int64_t)h * p.o_sh + kZ * zb +
+                               (int64_t)(row0 + 32 * (warp - R::kE0) + (lane >> 3)) * p.o_sl;
+            const int es = p.o_f32 ? 4 : 2;
+            // A thread holds a row, but stores that touch 32 rows at once keep the load-store unit
+            // from everybody else (2000 clocks a chunk): rows go through the chunk's Z tile, which
+            // nothing reads any more, and leave 128 bytes of 4 rows at a time.
+            const int q = lane & 7, r4 = lane >> 3;
+            unsigned char *o = static_cast<unsigned char *>(p.o) + at * es + 16 * q;
+            const int64_t step = (int64_t)dt * p.o_sl * es, row4 = 4 * p.o_sl * es;
+            const float *te = reinterpret_cast<const float *>(smem + M::oTe) + t;
+            const uint32_t zrow = (uint32_t)(M::kX + M::kY) + 128u * t;
+            const uint32_t zcol = (uint32_t)(M::kX + M::kY) + 128u * (32 * (warp - R::kE0) + r4);
+#pragma unroll 1
+            for (int c = 0; c < nc; ++c, o += step, ring.next()) {
+                const int b = c & 1, n = c == cpart ? npart : kC, nw = n - 32 * (warp - R::kE0) - r4;
+                const f2 rf = f2_splat(t < n ? te[rev ? kC - n : 0] : 0.0f);
+                const uint32_t oa = lanes + col_oa(b), ob = lanes + kColOb;
+                const uint32_t tile = sbase + (uint32_t)(ring.st * M::kStage);
+                // 128 bytes of every row from the tile to o, `off` bytes into the row; the tile is
+                // free as soon as it is read
+                auto copy_out = [&](int off, bool last) {
+                    __syncwarp();
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = lds128(tile + zcol + 512u * i + (uint32_t)((q ^ ((4 * i + r4) & 7)) << 4));
+                    if (last) fence_async_smem();  // (its next use is a copy's)
+                    __syncwarp();
+                    if (last && lane == 0) bar_arrive(bar(kBarZFree + ring.st));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (4 * i < nw && off + 16 * q < cols * es) *reinterpret_cast<uint4 *>(o + off + i * row4) = v[i];
+                };
                 if (!wait_all(kBarO + b, c >> 1)) break;
                 tc_after();
+                if (es == 2) {
+                    uint32_t r[kZ / 2];
+#pragma unroll
+                    for (int i = 0; i < kZ; i += 16) {
+                        float v[16], w[16];
+                        tmem_ld2x16(oa + (uint32_t)i, ob + (uint32_t)i, v, w);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2)
+                            r[(i + j) >> 1] = pack2(f2_fma(rf, f2_make(w[j], w[j + 1]), f2_make(v[j], v[j + 1])));
+                    }
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(kBarOFree + b));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sts128(tile + zrow + (uint32_t)((i ^ (t & 7)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                    copy_out(0, true);
+                } else {
 #pragma unroll 1
-                for (int i = 0; i < kZ; i += 16) {
-                    float v[16], ob[16];
-                    tmem_ld2x16(lanes + col_oa(b) + (uint32_t)i, lanes + kColOb + (uint32_t)i, v, ob);
+                    for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] = fmaf(rf, ob[j], v[j]);
+                        for (int i = 0; i < 32; i += 16) {
+                            float v[16], w[16];
+                            tmem_ld2x16(oa + (uint32_t)(32 * hf + i), ob + (uint32_t)(32 * hf + i), v, w);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 8)
-                        if (t < n && i + j < cols) {
-                            if (p.o_f32) {
-                                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at + i + j);
-                                o[0] = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                                o[1] = make_float4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
-                            } else {
-                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + at + i + j) =
-                                    make_uint4(pack2(v[j], v[j + 1]), pack2(v[j + 2], v[j + 3]), pack2(v[j + 4], v[j + 5]),
-                                               pack2(v[j + 6], v[j + 7]));
-                            }
+                            for (int j = 0; j < 16; j += 2)
+                                f2_split(f2_fma(rf, f2_make(w[j], w[j + 1]), f2_make(v[j], v[j + 1])), v[j], v[j + 1]);
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                sts128(tile + zrow + (uint32_t)((((i + j) >> 2) ^ (t & 7)) << 4), __float_as_uint(v[j]),
+                                       __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3]));
                         }
+                        if (hf == 1) {
+                            tc_before();
+                            __syncwarp();
+                            if (lane == 0) bar_arrive(bar(kBarOFree + b));
+                        }
+                        copy_out(128 * hf, hf == 1);
+                    }
                 }
-                tc_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(bar(kBarOFree + b));
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < R::kS0) {
         // ================================= group V =================================
-        const int gt = tid - 128;
+        constexpr int VT = 32 * R::kV, kItems = kC * 8 / VT / 2;  // 16-byte items a thread has in each half
+        const int gt = tid - 32 * R::kV0;
+        const uint32_t zs = sbase + M::oZs + 16u * gt;
+        const float *tv0 = reinterpret_cast<const float *>(smem + M::oTv) + (gt >> 3);
         bool ok = true;
-        for (int c = 0; c < nc && ok; ++c) {
-            const int st = c % NS, n = count_of(c);
-            if (!wait_all(kBarFull + st, c / NS)) break;
-            unsigned char *y = smem + st * M::kStage + M::kX, *z = y + M::kY, *zs = smem + M::oZs;
+#pragma unroll 1
+        for (int c = 0; c < nc && ok; ++c, ring.next()) {
+            const int st = ring.st, n = c == cpart ? npart : kC;
+            const uint32_t y = sbase + (uint32_t)(st * M::kStage + M::kX), z = y + M::kY + 16u * gt;
+            if (!wait_all(kBarZ + st, ring.use)) break;
             if (n < kC) {
                 // the rows behind the sequence, before any product reads them
+                if (!wait_all(kBarY + st, ring.use)) break;
 #pragma unroll 1
-                for (int i = n * 8 + gt; i < kC * 8; i += 128) {
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(z + 16 * i) = zero;
+                for (int i = n * 8 + gt; i < kC * 8; i += VT) {
+                    sts128(y + M::kY + 16 * i, 0, 0, 0, 0);
 #pragma unroll
-                    for (int j = 0; j < DX / 64; ++j) *reinterpret_cast<uint4 *>(y + j * 16384 + 16 * i) = zero;
+                    for (int j = 0; j < DX / 64; ++j) sts128(y + j * 16384 + 16 * i, 0, 0, 0, 0);
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(kBarClear));
             }
+            const float *tv = tv0 + (rev ? 0 : kC - n);
 #pragma unroll 1
             for (int hf = 0; hf < 2; ++hf) {
                 if (c > 0 && !(ok = wait_all(kBarZsFree + hf, c - 1))) break;
 #pragma unroll 1
-                for (int it = 0; it < 4; ++it) {
-                    const int i = hf * 512 + it * 128 + gt, row = i >> 3;
-                    uint4 hi, mid, lo;
+                for (int it = kItems * hf; it < kItems * (hf + 1); ++it) {
+                    // 8 columns of row VT / 8 it + gt / 8
+                    uint4 q = make_uint4(0, 0, 0, 0), hi, mid, lo;
                     float w = 0.0f;
-                    uint4 q = make_uint4(0, 0, 0, 0);
-                    if (row < n) {
-                        w = p.ws * pw[rev ? row + 1 : n - 1 - row];
-                        q = *reinterpret_cast<const uint4 *>(z + 16 * i);
+                    if (VT / 8 * it + (gt >> 3) < n) {
+                        w = tv[VT / 8 * it];
+                        q = lds128(z + 16u * VT * it);
                     }
-                    split3(w * bf16_lo(q.x), w * bf16_hi(q.x), hi.x, mid.x, lo.x);
-                    split3(w * bf16_lo(q.y), w * bf16_hi(q.y), hi.y, mid.y, lo.y);
-                    split3(w * bf16_lo(q.z), w * bf16_hi(q.z), hi.z, mid.z, lo.z);
-                    split3(w * bf16_lo(q.w), w * bf16_hi(q.w), hi.w, mid.w, lo.w);
-                    *reinterpret_cast<uint4 *>(zs + 16 * i) = hi;
-                    *reinterpret_cast<uint4 *>(zs + M::kZb + 16 * i) = mid;
-                    *reinterpret_cast<uint4 *>(zs + 2 * M::kZb + 16 * i) = lo;
+                    const f2 w2 = f2_splat(w);
+                    split3(w2, q.x, hi.x, mid.x, lo.x);
+                    split3(w2, q.y, hi.y, mid.y, lo.y);
+                    split3(w2, q.z, hi.z, mid.z, lo.z);
+                    split3(w2, q.w, hi.w, mid.w, lo.w);
+                    sts128(zs + 16u * VT * it, hi.x, hi.y, hi.z, hi.w);
+                    sts128(zs + 16u * VT * it + M::kZb, mid.x, mid.y, mid.z, mid.w);
+                    sts128(zs + 16u * VT * it + 2 * M::kZb, lo.x, lo.y, lo.z, lo.w);
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(kBarZs + hf));
+                if (lane == 0) {
+                    bar_arrive(bar(kBarZs + hf));
+                    if (hf == 1) bar_arrive(bar(kBarZFree + st));
+                }
             }
         }
-    } else if (warp < 12) {
+    } else {
         // ================================= group S =================================
         // dx <= 64: KV's second 64 rows repeat the first, so warps 2 and 3 take the
         // second 32 columns of rows 0..63
         constexpr int NCOL = DX == 64 ? 32 : 64;
-        const int w = warp - 8, row = (DX == 64 ? 32 * (w & 1) : 32 * w) + lane, c0 = DX == 64 ? 32 * (w >> 1) : 0;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-        float S[NCOL];
+        const int w = warp - R::kS0, row = (DX == 64 ? 32 * (w & 1) : 32 * w) + lane, c0 = DX == 64 ? 32 * (w >> 1) : 0;
+        const uint32_t kv = tmem + ((uint32_t)(32 * w) << 16) + kColKv + (uint32_t)c0;
+        f2 S[NCOL / 2];
         const int64_t blk = p.dx * (int64_t)p.dz;
-        {
-            const float *s0 = p.s0 ? p.s0 + ((int64_t)(p.s0_slot ? slot : pl.seq) * a.H + h) * blk : nullptr;
+        const float *s0 = (p.s0 && !kStates && row < p.dx)
+                              ? p.s0 + ((int64_t)(p.s0_slot ? slot : pl.seq) * a.H + h) * blk + row * p.s0_sr
+                              : nullptr;
 #pragma unroll
-            for (int i = 0; i < NCOL; ++i) {
-                const int col = kZ * zb + c0 + i;
-                S[i] = (s0 && !kStates && row < p.dx && col < p.dz) ? s0[row * p.s0_sr + col * p.s0_sc] : 0.0f;
-            }
+        for (int i = 0; i < NCOL; i += 2) {
+            const int col = kZ * zb + c0 + i;  // (dz is a multiple of 8)
+            const bool in = s0 && col < p.dz;
+            S[i / 2] = f2_make(in ? s0[col * p.s0_sc] : 0.0f, in ? s0[(col + 1) * p.s0_sc] : 0.0f);
         }
+        // lam^n S + KV as keep S + (part S + KV): with lam^n >= 1/2 part = lam^n - 1 keeps
+        // the bits of a slow decay over many chunks
+        const float m = expm1f((float)kC * g), mp = expm1f((float)npart * g);
+        const float keep = m >= -0.5f ? 1.0f : 0.0f, part = m >= -0.5f ? m : expf((float)kC * g);
+        const float keepp = mp >= -0.5f ? 1.0f : 0.0f, partp = mp >= -0.5f ? mp : expf((float)npart * g);
+        const uint32_t dst = sbase + M::oS + 128u * row;
+        const int x8 = row & 7, j0 = c0 >> 3;
         bool ok = true;
-        const float m128 = expm1f((float)kC * g);
+#pragma unroll 1
         for (int c = 0; c < nc; ++c) {
             if constexpr (!kStates) {
                 if (c > 0 && !(ok = wait_all(kBarOB, c - 1))) break;
-                unsigned char *dst = smem + M::oS + row * 128;
 #pragma unroll
                 for (int i = 0; i < NCOL; i += 8)
-                    *reinterpret_cast<uint4 *>(dst + ((((c0 + i) >> 3) ^ (row & 7)) << 4)) =
-                        make_uint4(pack2(S[i], S[i + 1]), pack2(S[i + 2], S[i + 3]), pack2(S[i + 4], S[i + 5]),
-                                   pack2(S[i + 6], S[i + 7]));
+                    sts128(dst + (uint32_t)(((j0 + (i >> 3)) ^ x8) << 4), pack2(S[i / 2]), pack2(S[i / 2 + 1]),
+                           pack2(S[i / 2 + 2]), pack2(S[i / 2 + 3]));
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(kBarS));
             }
+            const f2 k2 = f2_splat(c == cpart ? keepp : keep), p2 = f2_splat(c == cpart ? partp : part);
             if (!(ok = wait_all(kBarKV, c))) break;
             tc_after();
-            // lam^n S + KV as keep S + (part S + KV): with lam^n >= 1/2 part = lam^n - 1 keeps
-            // the bits of a slow decay over many chunks
-            const float m = count_of(c) == kC ? m128 : expm1f((float)count_of(c) * g);
-            const float keep = m >= -0.5f ? 1.0f : 0.0f, part = m >= -0.5f ? m : pw[count_of(c)];
 #pragma unroll
             for (int i = 0; i < NCOL; i += 8) {
                 float hi[8], mid[8], lo[8];
-                const uint32_t at = lanes + kColKv + (uint32_t)(c0 + i);
-                tmem_ld3x8(at, at + kZ, at + 2 * kZ, hi, mid, lo);
+                tmem_ld3x8(kv + i, kv + kZ + i, kv + 2 * kZ + i, hi, mid, lo);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    S[i + j] = fmaf(keep, S[i + j], fmaf(part, S[i + j], hi[j] + (mid[j] + lo[j])));
+                for (int j = 0; j < 8; j += 2) {
+                    f2 &v = S[(i + j) / 2];
+                    const f2 u = f2_add(f2_make(hi[j], hi[j + 1]), f2_add(f2_make(mid[j], mid[j + 1]), f2_make(lo[j], lo[j + 1])));
+                    v = f2_fma(k2, v, f2_fma(p2, v, u));
+                }
             }
             tc_before();
             __syncwarp();
@@ -665,13 +791,13 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_tc_kernel(const __grid_co
             float *f = p.fin + ((int64_t)(kStates ? slot : pl.seq) * a.H + h) * blk + row * (int64_t)p.dz + kZ * zb + c0;
 #pragma unroll
             for (int i = 0; i < NCOL; i += 4)
-                if (kZ * zb + c0 + i < p.dz) *reinterpret_cast<float4 *>(f + i) = make_float4(S[i], S[i + 1], S[i + 2], S[i + 3]);
+                if (kZ * zb + c0 + i < p.dz) *reinterpret_cast<ulonglong2 *>(f + i) = make_ulonglong2(S[i / 2], S[i / 2 + 1]);
         }
     }
 
     tc_before();
     __syncthreads();
-    if (warp == kQkWarp) {
+    if (warp == R::kQk) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
     }
@@ -791,7 +917,7 @@ cudaError_t launch_t(const TcArgs &a, const TcMaps &maps, int64_t slots, cudaStr
     if (e != cudaSuccess) return e;
     const int64_t grid = slots * a.H * a.units;
     if (grid > 0x7fffffffLL || a.seg <= 0) return cudaErrorInvalidConfiguration;
-    linattn_tc_kernel<DX, kStates><<<(unsigned)grid, kThreads, bytes, stream>>>(a, maps);
+    linattn_tc_kernel<DX, kStates><<<(unsigned)grid, Roles<DX>::kThreads, bytes, stream>>>(a, maps);
     return cudaGetLastError();
 }
 
