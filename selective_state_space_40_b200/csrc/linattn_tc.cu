@@ -34,8 +34,8 @@
 //            its bf16 form to the next chunk's O_b.
 //
 // Where sequences times heads leave SMs idle, sequences are cut into segments:
-// a first pass (kStates) forms each segment's own state from zero, a second
-// chains them, and the main pass starts every segment from its true state.
+// a first pass (kStates) forms each segment's own state from zero, and the main
+// pass starts every segment from the initial state and the earlier ones' own.
 // Every wait is bounded: a timeout sets MS_ERR_TIMEOUT and ends the CTA.
 
 #include <cuda.h>
@@ -78,10 +78,10 @@ struct TcProblem {
     int mx, my, mz;  // tensor maps of x, y, z
     int xg, yg, zg, dx, dz, rev, o_f32;
     float ws, ps, ro;
-    const float *s0;  // entering states: block (sequence or slot, head) of dx * dz, element (i, j) at i s0_sr + j s0_sc
-    float *fin;       // leaving states [batch, H, dx, dz], or (kStates) [slots, H, dx, dz]
-    int64_t s0_sr, s0_sc;
-    int s0_slot;
+    const float *s0;          // entering states: block (sequence, head) of dx * dz, element (i, j) at i s0_sr + j s0_sc
+    const float *seg_states;  // segments' own states, blocks (slot, head), or null
+    float *fin;               // leaving states [batch, H, dx, dz], or (kStates) [slots, H, dx, dz]
+    int64_t s0_sr, s0_sc, seg_sr, seg_sc;  // seg_states' strides
     void *o;
     int64_t o_sb, o_sl, o_sh;
     int nzb;          // blocks of kZ columns of z
@@ -739,17 +739,33 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
         const uint32_t kv = tmem + ((uint32_t)(32 * w) << 16) + kColKv + (uint32_t)c0;
         f2 S[NCOL / 2];
         const int64_t blk = p.dx * (int64_t)p.dz;
-        const float *s0 = (p.s0 && !kStates && row < p.dx)
-                              ? p.s0 + ((int64_t)(p.s0_slot ? slot : pl.seq) * a.H + h) * blk + row * p.s0_sr
-                              : nullptr;
+        {
+            const int64_t hb = (int64_t)h * blk, sb = a.H * blk;
+            auto add = [&](const float *from, int64_t sr, int64_t sc, float decay) {
+                const bool in = from && row < p.dx;
+                const int64_t at = row * sr + (kZ * zb + c0) * sc;
 #pragma unroll
-        for (int i = 0; i < NCOL; i += 2) {
-            const int col = kZ * zb + c0 + i;  // (dz is a multiple of 8)
-            const bool in = s0 && col < p.dz;
-            S[i / 2] = f2_make(in ? s0[col * p.s0_sc] : 0.0f, in ? s0[(col + 1) * p.s0_sc] : 0.0f);
+                for (int i = 0; i < NCOL; i += 2) {
+                    const bool use = in && kZ * zb + c0 + i < p.dz;  // (dz is a multiple of 8)
+                    const float u = use ? from[at + i * sc] : 0.0f, v = use ? from[at + (i + 1) * sc] : 0.0f;
+                    S[i / 2] = f2_fma(f2_splat(decay), S[i / 2], f2_make(u, v));
+                }
+            };
+#pragma unroll
+            for (int i = 0; i < NCOL / 2; ++i) S[i] = f2_splat(0.0f);
+            if constexpr (!kStates) {
+                add(p.s0 ? p.s0 + pl.seq * sb + hb : nullptr, p.s0_sr, p.s0_sc, 0.0f);
+                // the earlier segments' own states, in the order of work
+                if (p.seg_states)
+#pragma unroll 1
+                    for (int j = rev ? pl.ng - 1 : 0; j != pl.g; j += rev ? -1 : 1) {
+                        const int n = pl.len - j * a.seg < a.seg ? pl.len - j * a.seg : a.seg;
+                        add(p.seg_states + (int64_t)(slot - pl.g + j) * sb + hb, p.seg_sr, p.seg_sc, expf((float)n * g));
+                    }
+            }
         }
-        // lam^n S + KV as keep S + (part S + KV): with lam^n >= 1/2 part = lam^n - 1 keeps
-        // the bits of a slow decay over many chunks
+        // lam^n S as keep S + part S, rounded once: with lam^n >= 1/2 part = lam^n - 1 keeps the
+        // bits of a slow decay over many chunks
         const float m = expm1f((float)kC * g), mp = expm1f((float)npart * g);
         const float keep = m >= -0.5f ? 1.0f : 0.0f, part = m >= -0.5f ? m : expf((float)kC * g);
         const float keepp = mp >= -0.5f ? 1.0f : 0.0f, partp = mp >= -0.5f ? mp : expf((float)npart * g);
@@ -768,7 +784,10 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
                 __syncwarp();
                 if (lane == 0) bar_arrive(bar(kBarS));
             }
+            // lam^n S while KV is formed (before the wait: KV's columns are needed for the next chunk)
             const f2 k2 = f2_splat(c == cpart ? keepp : keep), p2 = f2_splat(c == cpart ? partp : part);
+#pragma unroll
+            for (int i = 0; i < NCOL / 2; ++i) S[i] = f2_fma(p2, S[i], f2_mul(k2, S[i]));
             if (!(ok = wait_all(kBarKV, c))) break;
             tc_after();
 #pragma unroll
@@ -776,11 +795,9 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
                 float hi[8], mid[8], lo[8];
                 tmem_ld3x8(kv + i, kv + kZ + i, kv + 2 * kZ + i, hi, mid, lo);
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    f2 &v = S[(i + j) / 2];
-                    const f2 u = f2_add(f2_make(hi[j], hi[j + 1]), f2_add(f2_make(mid[j], mid[j + 1]), f2_make(lo[j], lo[j + 1])));
-                    v = f2_fma(k2, v, f2_fma(p2, v, u));
-                }
+                for (int j = 0; j < 8; j += 2)
+                    S[(i + j) / 2] = f2_add(S[(i + j) / 2], f2_add(f2_make(hi[j], hi[j + 1]),
+                                                                   f2_add(f2_make(mid[j], mid[j + 1]), f2_make(lo[j], lo[j + 1]))));
             }
             tc_before();
             __syncwarp();
@@ -800,41 +817,6 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
     if (warp == R::kQk) {
         tc_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
-    }
-}
-
-// The states that segments start from, in place of what each contributes:
-// st[j] <- lam^(tokens before it) s0 + the earlier segments' parts, in order.
-struct ChainArgs {
-    float *st[2];
-    const float *s0[2];
-    int64_t s0_sr[2], s0_sc[2];
-    int dx[2], dz[2], rev[2];
-};
-__global__ void __launch_bounds__(256) linattn_chain_kernel(const __grid_constant__ TcArgs a, const ChainArgs ch) {
-    const int k = blockIdx.z;
-    const int64_t seq = (int)blockIdx.y / a.H, h = (int)blockIdx.y % a.H, blk = (int64_t)ch.dx[k] * ch.dz[k];
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    int64_t base = seq * a.nseg, len = a.seqlen;
-    if (a.seq_start) {
-        const int64_t s = a.seq_start[seq], t = a.seq_start[seq + 1];
-        if (!(s >= 0 && t >= s && t <= a.total)) return;
-        base = s / a.seg + seq;
-        len = t - s;
-    }
-    if (e >= blk) return;
-    const int64_t ng = len > a.seg ? (len + a.seg - 1) / a.seg : 1;
-    const float g = fmaxf(__ldg(a.log_decay + h), -1e30f);
-    const int64_t i = e / ch.dz[k], j = e % ch.dz[k];
-    float S = ch.s0[k] ? ch.s0[k][(seq * a.H + h) * blk + i * ch.s0_sr[k] + j * ch.s0_sc[k]] : 0.0f;
-    float *st = ch.st[k] + h * blk + e;
-    for (int64_t c = 0; c < ng; ++c) {
-        const int64_t q = ch.rev[k] ? ng - 1 - c : c;
-        float *at = st + (base + q) * a.H * blk;
-        const float own = c < ng - 1 ? *at : 0.0f;
-        *at = S;
-        const int64_t left = len - q * a.seg, n = left < a.seg ? left : a.seg;
-        S = fmaf(expf((float)n * g), S, own);
     }
 }
 
@@ -942,7 +924,8 @@ size_t linattn_tc_workspace(int64_t batch, int64_t rows, bool packed, int64_t H,
     if (batch < 1 || rows < 1) return 0;
     const int units = bwd ? 2 * zblocks(dk) + zblocks(dv) : zblocks(dv);
     const SegPlan s = seg_plan(batch, rows, packed, H, units, num_sms);
-    return s.segmented ? (size_t)(bwd ? 2 : 1) * (size_t)s.slots * H * dk * dv * sizeof(float) : 0;
+    // (forward: and a copy of the initial states, for a call that overwrites them)
+    return s.segmented ? (size_t)(bwd ? 2 * s.slots : s.slots + batch) * H * dk * dv * sizeof(float) : 0;
 }
 
 cudaError_t launch_linattn_tc(const LaArgs &la, void *workspace, int num_sms, cudaStream_t stream) {
@@ -985,35 +968,32 @@ cudaError_t launch_linattn_tc(const LaArgs &la, void *workspace, int num_sms, cu
     a.segmented = sp.segmented ? 1 : 0;
     if (sp.segmented) {
         // the segments' own states: of the forward direction (problem 0), and of the reverse one
-        // (problem 2; problem 1 reads it with rows and columns exchanged)
+        // (problem 2; problem 1 reads it with rows and columns exchanged, as it does dfinal)
         TcArgs s = a;
-        ChainArgs ch{};
         float *st = static_cast<float *>(workspace);
-        const int own[2] = {0, 2};
         s.np = la.np == 1 ? 1 : 2;
         s.units = 0;
         for (int k = 0; k < s.np; ++k) {
-            const TcProblem &p = a.p[own[k]];
+            const TcProblem &p = a.p[2 * k];
             s.p[k] = p;
             s.p[k].fin = st + k * sp.slots * la.H * p.dx * p.dz;
             s.units += p.nzb;
-            ch.st[k] = s.p[k].fin;
-            ch.s0[k] = p.s0; ch.s0_sr[k] = p.s0_sr; ch.s0_sc[k] = p.s0_sc;
-            ch.dx[k] = p.dx; ch.dz[k] = p.dz; ch.rev[k] = p.rev;
         }
-        cudaError_t e = dxmax <= 64 ? launch_t<64, true>(s, maps, sp.slots, stream)
-                                    : launch_t<128, true>(s, maps, sp.slots, stream);
-        if (e != cudaSuccess) return e;
-        const dim3 grid((unsigned)((ch.dx[0] * ch.dz[0] + 255) / 256), (unsigned)(la.batch * la.H), (unsigned)s.np);
-        linattn_chain_kernel<<<grid, 256, 0, stream>>>(a, ch);
-        e = cudaGetLastError();
+        const cudaError_t e = dxmax <= 64 ? launch_t<64, true>(s, maps, sp.slots, stream)
+                                          : launch_t<128, true>(s, maps, sp.slots, stream);
         if (e != cudaSuccess) return e;
         for (int i = 0; i < la.np; ++i) {
-            TcProblem &t = a.p[i];
-            t.s0 = ch.st[i == 0 ? 0 : 1];
-            t.s0_slot = 1;
-            t.s0_sr = i == 1 ? 1 : t.dz;
-            t.s0_sc = i == 1 ? t.dx : 1;
+            a.p[i].seg_states = s.p[i == 0 ? 0 : 1].fin;
+            a.p[i].seg_sr = i == 1 ? 1 : a.p[i].dz;
+            a.p[i].seg_sc = i == 1 ? a.p[i].dx : 1;
+        }
+        if (a.p[0].s0 && a.p[0].s0 == a.p[0].fin) {
+            // a sequence's last segment may end before its others begin
+            const size_t n = (size_t)la.batch * la.H * a.p[0].dx * a.p[0].dz;
+            float *copy = st + (size_t)sp.slots * la.H * a.p[0].dx * a.p[0].dz;
+            const cudaError_t ec = cudaMemcpyAsync(copy, a.p[0].s0, n * sizeof(float), cudaMemcpyDeviceToDevice, stream);
+            if (ec != cudaSuccess) return ec;
+            a.p[0].s0 = copy;
         }
     }
     return dxmax <= 64 ? launch_t<64, false>(a, maps, sp.slots, stream) : launch_t<128, false>(a, maps, sp.slots, stream);
