@@ -17,25 +17,32 @@
 // is handed on for as long as lam remembers; S rounded to bf16 where X reads
 // it, never where it is kept.
 //
-// A CTA owns one (segment of a sequence, head, 64 columns of z) and walks its
-// chunks with the state in registers. What bounds it is shared memory: a chunk
-// moves some 370 KB of it at dx = 128 (operands of the products 208, tensor
-// copies 80, Z' 64, S 16), 2900 clocks at 128 bytes a clock, so KV takes the three
-// parts of Z' as one product of N = 192 (24 products of N = 64 read Y three times,
-// and took 1900 clocks a chunk against 800). The roles run on different chunks at
-// the same time, each warp waiting for its own inputs only:
-//   one warp loads (tensor copies, 128-byte swizzle, NS stages); one warp each
-//   issues QK, KV, and O_a with O_b;
+// An item is one (segment of a sequence, head, 64 columns of z); a CTA walks its
+// chunks with the state in registers. The kernel is persistent, one CTA per SM, and
+// its roles run on from one item into the next, so a CTA's set-up and the filling
+// of its pipeline are paid once. The roles, each waiting for its own inputs only:
+//   one warp finds the items, lays out what they need and loads their tiles (tensor
+//   copies, 128-byte swizzle, NS stages); one warp each issues QK, KV, and O_a with O_b;
 //   group P  weights QK into P (tensor memory, in place);
 //   group E  adds up O_a and lam^.. O_b and writes o;
 //   group V  forms Z', and clears the rows of a chunk's Y and Z that are behind
 //            the sequence;
 //   group S  keeps S (a thread: one row, or half of one), adds KV, and hands
 //            its bf16 form to the next chunk's O_b.
+// KV takes the three parts of Z' as one product of N = 192 (24 products of N = 64
+// read Y three times, and took 1900 clocks a chunk against 1200).
 //
-// Where sequences times heads leave SMs idle, sequences are cut into segments:
-// a first pass (kStates) forms each segment's own state from zero, and the main
-// pass starts every segment from the initial state and the earlier ones' own.
+// Three ways to cut the work, by the number of (sequence, head, column block)s, each
+// of which is a chain of chunks (see plan_of):
+//   kWhole    an item is a whole sequence;
+//   kChained  a sequence is several items, and the state goes from one to the next
+//             through the workspace: items are claimed in ticket order, all first
+//             segments before all second ones, so an item's predecessor was claimed
+//             before it and mostly has ended, and every wait ends. Evens out chains
+//             that do not divide by the SMs.
+//   kStates   too few chains to fill the SMs: a first pass forms each segment's own
+//             state from zero, and the main pass starts every segment from the initial
+//             state and the earlier ones' own.
 // Every wait is bounded: a timeout sets MS_ERR_TIMEOUT and ends the CTA.
 
 #include <cuda.h>
@@ -66,7 +73,8 @@ struct Roles {
     static constexpr int kLoad = kE0 + 4, kQk = kLoad + 1, kKv = kLoad + 2, kO = kLoad + 3;
     static constexpr int kThreads = 32 * (kO + 1);
 };
-constexpr uint32_t kSpinTries = 1u << 20;
+constexpr uint32_t kSpinTries = 1u << 20;   // tries of a barrier
+constexpr uint32_t kFlagTries = 1u << 22;   // polls of a predecessor's flag
 
 // tensor memory: two buffers of QK (P takes its first 64 columns, O_a its last
 // 64), O_b, and the three parts of KV
@@ -80,21 +88,24 @@ struct TcProblem {
     float ws, ps, ro;
     const float *s0;          // entering states: block (sequence, head) of dx * dz, element (i, j) at i s0_sr + j s0_sc
     const float *seg_states;  // segments' own states, blocks (slot, head), or null
-    float *fin;               // leaving states [batch, H, dx, dz], or (kStates) [slots, H, dx, dz]
+    float *fin;               // leaving states [batch, H, dx, dz], or (first pass of kStates) [slots, H, dx, dz]
     int64_t s0_sr, s0_sc, seg_sr, seg_sc;  // seg_states' strides
     void *o;
     int64_t o_sb, o_sl, o_sh;
     int nzb;          // blocks of kZ columns of z
 };
+enum { kWhole = 0, kChained = 1, kStates = 2 };
 struct TcArgs {
     const float *log_decay;
     const int32_t *seq_start;
     int *status;
     int batch, seqlen, total, H;
-    int seg;   // tokens per segment (a multiple of kC)
-    int nseg;  // segments per sequence (dense); slots of the packed case are numbered below
-    int segmented;
+    int seg;    // tokens per segment (a multiple of kC)
+    int nseg;   // segments per sequence (dense)
     int np, units;  // units: sum of nzb
+    // kChained: the ticket, a flag per chain (warps of group S that have handed its state on), the states
+    int *ticket, *flags;
+    float *chain;
     TcProblem p[kLaMaxProblems];
 };
 struct TcMaps {
@@ -102,22 +113,32 @@ struct TcMaps {
 };
 
 // shared memory (bytes)
-template <int DX, bool kStates>
+// what the roles need of an item
+struct Item {
+    int valid, seq, h, pi, zb;
+    int row0, nc;      // the first row of chunk c is row0 + c * (rev ? -kC : kC)
+    int cpart, npart;  // the chunk that is not full (-1: none), and its tokens
+    int j, last;       // segment in the order of work, and whether it is the last of them
+    int slot0;         // number of the sequence's first segment
+    int ng, len;       // the sequence's segments and tokens
+    int unit, pad;
+};
+template <int DX, bool kOwn>
 struct Smem {
-    static constexpr int kX = kStates ? 0 : kC * DX * 2;
+    static constexpr int kX = kOwn ? 0 : kC * DX * 2;
     static constexpr int kY = kC * DX * 2;
     static constexpr int kZb = kC * kZ * 2;
     static constexpr int kStage = kX + kY + kZb;
     static constexpr int kStages = DX == 64 ? 3 : 2;
-    static constexpr int oZs = kStages * kStage;             // three parts of Z'
-    static constexpr int oS = oZs + 3 * kZb;                 // S in bf16
-    static constexpr int oTv = oS + (kStates ? 0 : DX * kZ * 2);  // weights of Z's rows
-    static constexpr int oTe = oTv + 128 * 4;                // of O_b's rows
-    static constexpr int oPs = oTe + 128 * 4;                // ps lam^n
-    static constexpr int oDiag = oPs + 128 * 4;              // ps lam^|d| at 31 + d, d = t - s, 0 on the masked side
-    static constexpr int oCf = oDiag + 64 * 4;               // lam^(31-c), in reverse lam^c, c < 32
-    static constexpr int oBar = oCf + 32 * 4;
-    static constexpr int kBytes = oBar + 8 * 38 + 16;
+    static constexpr int oZs = kStages * kStage;               // three parts of Z'
+    static constexpr int oS = oZs + 3 * kZb;                   // S in bf16
+    static constexpr int oItem = oS + (kOwn ? 0 : DX * kZ * 2);  // two items
+    // two items' tables: lam^n, n = 0..128; lam^|d| at 31 + d, d = t - s, 0 on the masked side;
+    // lam^(31-c), in reverse lam^c, c < 32
+    static constexpr int oTab = oItem + 2 * (int)sizeof(Item);
+    static constexpr int kPw = 0, kDiag = 132, kCf = kDiag + 64, kTab = kCf + 32;  // floats
+    static constexpr int oBar = oTab + 2 * kTab * 4;
+    static constexpr int kBytes = oBar + 8 * 46 + 16;
 };
 enum {
     kBarX = 0,        // [3] a stage's X, Y, Z tiles are in
@@ -136,9 +157,11 @@ enum {
     kBarKVFree = 31,  // group S has read it
     kBarS = 32,       // S is in shared memory
     kBarOB = 33,      // O_b is done (and S read)
-    kBarClear = 34,   // the rows behind the sequence are cleared (once, in the chunk that has some)
-    kBarEnd = 35,     // [3] nothing of an issuing warp is in flight
-    kNumBars = 38
+    kBarClear = 34,   // [3] the rows behind the sequence are cleared (of a stage's chunk that has some)
+    kBarItem = 37,    // [2] an item is laid out
+    kBarItemFree = 39,  // [2] every role is done with it
+    kBarEnd = 41,     // [3] nothing of an issuing warp is in flight
+    kNumBars = 44
 };
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -174,6 +197,16 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t ta, uint64_t db, uin
         :
         : "r"(d), "r"(ta), "l"(db), "r"(id), "r"(acc ? 1u : 0u)
         : "memory");
+}
+// One lane of the warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0u;
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -288,120 +321,139 @@ __device__ __forceinline__ uint32_t pack2(f2 v) {
     return pack2(a, b);
 }
 __device__ __forceinline__ f2 unpack2(uint32_t v) { return f2_make(bf16_lo(v), bf16_hi(v)); }
-// w q = hi + mid + lo in bf16 parts (24 significant bits) for a pair q of bf16
+// The upper halves of a pair: bf16 where the lower ones are zero, else cut off.
+__device__ __forceinline__ uint32_t halves2(f2 v) {
+    float a, b;
+    f2_split(v, a, b);
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ f2 cut2(f2 v) {
+    float a, b;
+    f2_split(v, a, b);
+    return f2_make(__uint_as_float(__float_as_uint(a) & 0xffff0000u), __uint_as_float(__float_as_uint(b) & 0xffff0000u));
+}
+// w q = hi + mid + lo in bf16 parts for a pair q of bf16: cutting off takes the 24
+// bits apart exactly, 8 at a time, without the conversions (their pipe was 89 % busy
+// with them, and the kernel took NNN times as long).
 __device__ __forceinline__ void split3(f2 w, uint32_t q, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    f2 v = f2_mul(w, unpack2(q));
-    hi = pack2(v);
-    v = f2_sub(v, unpack2(hi));
-    mid = pack2(v);
-    lo = pack2(f2_sub(v, unpack2(mid)));
+    f2 v = f2_mul(w, unpack2(q)), t = cut2(v);
+    hi = halves2(t);
+    v = f2_sub(v, t);
+    t = cut2(v);
+    mid = halves2(t);
+    lo = halves2(f2_sub(v, t));
 }
 
-// The sequence and segment of a slot. Slot numbers: dense, sequence * nseg +
-// segment; packed, floor(first row / seg) + sequence + segment, which gives each
-// sequence as many numbers as it has segments or more. Every lane returns the same.
-struct Place {
-    int seq, g, row0, len, ng;
-    bool ok, bad;  // a segment of the sequence; offsets out of order
-};
-__device__ __forceinline__ Place place_of(const TcArgs &a, int slot, int lane) {
-    Place p{};
-    int64_t len = a.seqlen;
-    if (a.seq_start == nullptr) {
-        p.seq = slot / a.nseg;
-        p.g = slot % a.nseg;
-    } else {
-        p.seq = slot;
-        if (a.segmented) {
-            // the last sequence whose first slot is not behind this one
-            int base = 0;
-            p.seq = 0;
-            for (int i0 = 0; i0 < a.batch; i0 += 32) {
-                const int i = i0 + lane;
-                const int bi = i < a.batch ? a.seq_start[i] / a.seg + i : INT_MAX;
-                const unsigned m = __ballot_sync(0xffffffffu, bi <= slot);
-                if (m == 0u) break;
-                const int last = 31 - __clz(m);
-                p.seq = i0 + last;
-                base = __shfl_sync(0xffffffffu, bi, last);
-            }
-            p.g = slot - base;
-        }
-        const int64_t s = a.seq_start[p.seq], e = a.seq_start[p.seq + 1];
-        p.row0 = (int)s;
-        len = e - s;
-        p.bad = !(s >= 0 && e >= s && e <= a.total);
-    }
-    p.len = p.bad ? 0 : (int)len;
-    p.ng = p.len > a.seg ? (p.len + a.seg - 1) / a.seg : 1;
-    p.ok = !p.bad && p.g >= 0 && p.g < p.ng;
-    return p;
+__device__ __forceinline__ int ld_acquire(const int *p) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
 }
+
+// Segments of sequence i (0 where its offsets are out of order), its first row,
+// length, and the number of its first segment's slot: dense, i * nseg; packed,
+// floor(first row / seg) + i, which gives each sequence as many numbers as it has
+// segments or more.
+__device__ __forceinline__ int segments_of(const TcArgs &a, int i, int &row0, int &len, int &slot0) {
+    row0 = 0;
+    len = a.seqlen;
+    slot0 = i * a.nseg;
+    if (a.seq_start) {
+        const int s = a.seq_start[i], e = a.seq_start[i + 1];
+        if (s < 0 || e < s || e > a.total) return 0;
+        row0 = s;
+        len = e - s;
+        slot0 = s / a.seg + i;
+    }
+    return len > a.seg ? (len - 1) / a.seg + 1 : 1;
+}
+
+// The items in their order: all sequences' first segments (in the order of work),
+// then all second ones, and so on; within, sequence, head, unit. The first pass of
+// kStates leaves out each sequence's last. A warp asks for increasing numbers, and
+// gets the same answer in every lane.
+template <bool kOwn>
+struct Finder {
+    int j = 0, before = 0;  // packed: the level, and the (sequence, segment)s before it
+    __device__ __forceinline__ bool find(const TcArgs &a, int n, int lane, Item &it) {
+        it.unit = n % a.units;
+        n /= a.units;
+        it.h = n % a.H;
+        n /= a.H;
+        int row0, len, slot0, ng;
+        if (a.seq_start == nullptr) {
+            it.seq = n % a.batch;
+            j = n / a.batch;
+            if (j >= a.nseg - (kOwn ? 1 : 0)) return false;
+        } else {
+            for (;; ++j) {
+                int k = n - before, count = 0;
+                it.seq = -1;
+                for (int i0 = 0; i0 < a.batch; i0 += 32) {
+                    const int i = i0 + lane;
+                    const unsigned m =
+                        __ballot_sync(0xffffffffu, i < a.batch && segments_of(a, i, row0, len, slot0) - (kOwn ? 1 : 0) > j);
+                    if (it.seq < 0 && k < __popc(m)) it.seq = i0 + (int)__fns(m, 0, k + 1);
+                    k -= __popc(m);
+                    count += __popc(m);
+                }
+                if (it.seq >= 0) break;
+                if (count == 0) return false;
+                before += count;
+            }
+        }
+        ng = segments_of(a, it.seq, row0, len, slot0);
+        int zb = it.unit, pi = 0;
+        while (zb >= a.p[pi].nzb) zb -= a.p[pi++].nzb;
+        const bool rev = a.p[pi].rev != 0;
+        const int seg0 = (rev ? ng - 1 - j : j) * a.seg;
+        const int ntok = len - seg0 < a.seg ? len - seg0 : a.seg;
+        it.pi = pi;
+        it.zb = zb;
+        it.nc = (ntok + kC - 1) / kC;
+        it.npart = ntok % kC == 0 ? kC : ntok % kC;
+        it.cpart = it.npart == kC ? -1 : rev ? 0 : it.nc - 1;
+        it.row0 = row0 + seg0 + (rev && it.nc > 0 ? (it.nc - 1) * kC : 0);
+        it.j = j;
+        it.last = j == ng - 1;
+        it.slot0 = slot0;
+        it.ng = ng;
+        it.len = len;
+        return true;
+    }
+};
 
 // The roles' code is what the SM's instruction cache has to hold at once (five
 // groups of warps, each in a loop of its own): with the loops unrolled and the
 // call's parameters read inside them, warps waited for instructions half of the
 // time. So what a chunk needs is laid out before the loops (tables, addresses,
 // steps), and the loops are short.
-template <int DX, bool kStates>
+template <int DX, bool kOwn, int kMode>
 __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcArgs a,
                                                                  const __grid_constant__ TcMaps maps) {
-    using M = Smem<DX, kStates>;
+    using M = Smem<DX, kOwn>;
     using R = Roles<DX>;
     constexpr int NS = M::kStages, KX = DX / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be the same in all lanes)
     const uint32_t sbase = saddr(smem);
-    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * 38);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * 46);
     volatile uint32_t *abort_flag = misc + 1;
+    Item *items = reinterpret_cast<Item *>(smem + M::oItem);
+    float *tabs = reinterpret_cast<float *>(smem + M::oTab);
 
-    int unit = (int)(blockIdx.x % (unsigned)a.units);
-    const int hs = (int)(blockIdx.x / (unsigned)a.units), h = hs % a.H, slot = hs / a.H;
-    int pi = 0;
-    while (unit >= a.p[pi].nzb) unit -= a.p[pi++].nzb;
-    const TcProblem &p = a.p[pi];
-    const int zb = unit;
-    const Place pl = place_of(a, slot, lane);
-    if (pl.bad && tid == 0 && a.status) atomicOr(a.status, MS_ERR_SHAPE);
-    const bool rev = p.rev != 0;
-    if (!pl.ok || (kStates && (rev ? pl.g == 0 : pl.g == pl.ng - 1))) return;
-    const int seg0 = pl.g * a.seg;
-    const int ntok = pl.len - seg0 < a.seg ? pl.len - seg0 : a.seg;
-    const int nc = (ntok + kC - 1) / kC;
-    // the chunk (in the order of work) that is not full, if one is not, and its tokens
-    const int npart = ntok % kC == 0 ? kC : ntok % kC, cpart = npart == kC ? -1 : rev ? 0 : nc - 1;
-    // the first row of chunk c is row0 + c * dt
-    const int dt = rev ? -kC : kC, row0 = pl.row0 + seg0 + (rev ? (nc - 1) * kC : 0);
-
-    const float g = fmaxf(__ldg(a.log_decay + h), -1e30f);  // -inf: 0 * -inf must be 0
-    if (tid < kC) {
-        float *tv = reinterpret_cast<float *>(smem + M::oTv), *te = reinterpret_cast<float *>(smem + M::oTe);
-        float *ps = reinterpret_cast<float *>(smem + M::oPs), *dg = reinterpret_cast<float *>(smem + M::oDiag);
-        float *cf = reinterpret_cast<float *>(smem + M::oCf);
-        const float w = expf((float)tid * g), w1 = expf((float)(tid + 1) * g);
-        if (rev) {
-            tv[tid] = p.ws * w1;
-            te[kC - 1 - tid] = p.ro * w;
-        } else {
-            tv[kC - 1 - tid] = p.ws * w;
-            te[tid] = p.ro * w1;
-        }
-        ps[tid] = p.ps * w;
-        if (tid < 32) {
-            dg[31 + tid] = rev && tid > 0 ? 0.0f : p.ps * w;
-            if (tid > 0) dg[31 - tid] = rev ? p.ps * w : 0.0f;
-            cf[rev ? tid : 31 - tid] = w;
-        }
-    }
     const uint32_t bars = sbase + (uint32_t)M::oBar;
     if (tid == 0) {
         for (int i = 0; i < kNumBars; ++i) {
-            const bool warps4 = (i >= kBarP && i < kBarP + 2) || (i >= kBarOFree && i < kBarOFree + 2) ||
-                                i == kBarKVFree || i == kBarS;
-            const bool warpsv = (i >= kBarZs && i < kBarZs + 2) || i == kBarClear;
-            const bool two = (i >= kBarXFree && i < kBarYFree) || (i >= kBarYFree && i < kBarZFree && !kStates);
-            const bool zfree = i >= kBarZFree && i < kBarZFree + 3;  // the warps of V and E
-            bar_init(bars + 8 * i, warps4 ? 4 : warpsv ? R::kV : two ? 2 : zfree ? (kStates ? R::kV : R::kV + 4) : 1);
+            int n = 1;
+            if (i >= kBarXFree && i < kBarYFree) n = 2;
+            else if (i >= kBarYFree && i < kBarZFree) n = kOwn ? 1 : 2;
+            else if (i >= kBarZFree && i < kBarQK) n = kOwn ? R::kV : R::kV + 4;  // the warps of V and E
+            else if ((i >= kBarP && i < kBarO) || (i >= kBarOFree && i < kBarZs) || i == kBarKVFree || i == kBarS) n = 4;
+            else if ((i >= kBarZs && i < kBarZsFree) || (i >= kBarClear && i < kBarItem)) n = R::kV;
+            else if (i >= kBarItemFree && i < kBarEnd) n = kOwn ? R::kV + 5 : R::kV + 15;  // every role's warps
+            bar_init(bars + 8 * i, n);
         }
         misc[1] = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -414,13 +466,14 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
     tc_before();
     __syncthreads();
     tc_after();
-    const uint32_t tmem = misc[0];
+    const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
     auto wait = [&](int i, int k) { return bar_wait(bar(i), (uint32_t)k, abort_flag, a.status); };
     auto wait_all = [&](int i, int k) { return __all_sync(0xffffffffu, wait(i, k)) != 0; };  // whole warps: one answer
-    // every product that an issuing thread has in flight completes before the tensor memory is freed
+    // every product that an issuing warp has in flight completes before the tensor memory is freed
     auto drain = [&](int i) {
-        mma_commit(bar(kBarEnd + i));
+        if (elect_one()) mma_commit(bar(kBarEnd + i));
+        __syncwarp();
         for (uint32_t k = 0; k < kSpinTries && !bar_try(bar(kBarEnd + i), 0u); ++k) {}
     };
     // stages go round: st = c % NS, and use = c / NS counts the rounds
@@ -431,305 +484,396 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
         }
     } ring;
 
-    if (warp == R::kLoad) {
-        if (lane == 0) {
-            const CUtensorMap *mx = &maps.m[p.mx], *my = &maps.m[p.my], *mz = &maps.m[p.mz];
-            const int b = a.seq_start ? 0 : pl.seq;
-            const int hx = h / p.xg, hy = h / p.yg, hz = h / p.zg;
-            int c = 0, t = row0, sent_of_last = 0;  // sent_of_last: of the chunk at which the loop stopped
-            bool ok = true;
+    // The items one after another: wait for one, read it, run `body`, let it go.
+    // cc counts a role's chunks over all items: barriers go by it.
+    int cc = 0;
+    auto each_item = [&](auto body) {
 #pragma unroll 1
-            for (; c < nc; ++c, t += dt, ring.next()) {
-                const int st = ring.st, use = ring.use;
-                const uint32_t dst = sbase + (uint32_t)(st * M::kStage);
-                sent_of_last = 0;
-                if (use > 0 && !(ok = wait(kBarYFree + st, use - 1))) break;
-                bar_arrive_tx(bar(kBarY + st), (uint32_t)M::kY);
-#pragma unroll
-                for (int i = 0; i < DX / 64; ++i) tma_load4(my, dst + M::kX + i * 16384, bar(kBarY + st), 64 * i, hy, t, b);
-                sent_of_last = 1;
-                if (use > 0 && !(ok = wait(kBarZFree + st, use - 1))) break;
-                bar_arrive_tx(bar(kBarZ + st), (uint32_t)M::kZb);
-                tma_load4(mz, dst + M::kX + M::kY, bar(kBarZ + st), kZ * zb, hz, t, b);
-                sent_of_last = 2;
-                if constexpr (!kStates) {
-                    if (use > 0 && !(ok = wait(kBarXFree + st, use - 1))) break;
-                    bar_arrive_tx(bar(kBarX + st), (uint32_t)M::kX);
-#pragma unroll
-                    for (int i = 0; i < DX / 64; ++i) tma_load4(mx, dst + i * 16384, bar(kBarX + st), 64 * i, hx, t, b);
-                }
-            }
-            // when stopping, the copies issued have landed before the CTA ends
-            for (int q = 0; q < 3 && !ok; ++q) {
-                const int at = q == 0 ? kBarY : q == 1 ? kBarZ : kBarX, last = q < sent_of_last ? c : c - 1;
-                for (int i = last < NS ? 0 : last - NS + 1; i <= last && (q < 2 || !kStates); ++i)
-                    for (uint32_t k = 0; k < kSpinTries && !bar_try(bar(at + i % NS), (uint32_t)(i / NS) & 1u); ++k) {}
-            }
+        for (int i = 0;; ++i) {
+            if (!wait_all(kBarItem + (i & 1), i >> 1)) return false;
+            const Item &it = items[i & 1];
+            if (!it.valid) return true;
+            if (!body(it, tabs + (i & 1) * M::kTab)) return false;
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(kBarItemFree + (i & 1)));
         }
-    } else if (warp == R::kQk) {
-        if constexpr (!kStates) {
-            if (lane == 0) {
-                const uint64_t dx0 = sdesc(sbase, 0), dy0 = sdesc(sbase + M::kX, 0);
-#pragma unroll 1
-                for (int c = 0; c < nc; ++c, ring.next()) {
-                    const int b = c & 1, st = ring.st;
-                    if (!wait(kBarX + st, ring.use) || !wait(kBarY + st, ring.use) || (c == cpart && !wait(kBarClear, 0)) ||
-                        (c >= 2 && !wait(kBarOFree + b, (c - 2) >> 1)))
-                        break;
-                    tc_after();
-                    const uint64_t x = dstep(dx0, st * M::kStage), y = dstep(dy0, st * M::kStage);
-#pragma unroll
-                    for (int k = 0; k < KX; ++k) {
-                        const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
-                        mma(tmem + col_qk(b), dstep(x, off), dstep(y, off), idesc(kC, false, false), k > 0);
-                    }
-                    mma_commit(bar(kBarQK + b));
-                    mma_commit(bar(kBarXFree + st));
-                    mma_commit(bar(kBarYFree + st));
-                }
-                drain(0);
+    };
+
+    if (warp == R::kLoad) {
+        // ============================ items and loads ============================
+        if (blockIdx.x == 0 && a.seq_start && a.status)
+            for (int i = lane; i < a.batch; i += 32) {
+                int row0, len, slot0;
+                if (segments_of(a, i, row0, len, slot0) == 0) atomicOr(a.status, MS_ERR_SHAPE);
             }
+        Finder<kOwn> finder;
+        bool ok = true;
+        int sent[3] = {0, 0, 0};  // copies of Y, Z, X issued
+        int ticket = 0, next = 0;
+        if (kMode == kChained && lane == 0) next = atomicAdd(a.ticket, 1);
+#pragma unroll 1
+        for (int i = 0; ok; ++i) {
+            if (kMode == kChained) {
+                ticket = __shfl_sync(0xffffffffu, next, 0);
+                if (lane == 0) next = atomicAdd(a.ticket, 1);
+            } else {
+                ticket = (int)(blockIdx.x + (unsigned)i * gridDim.x);
+            }
+            Item it;
+            const bool valid = finder.find(a, ticket, lane, it);
+            it.valid = valid ? 1 : 0;
+            if (i >= 2) ok = __all_sync(0xffffffffu, wait(kBarItemFree + (i & 1), (i >> 1) - 1)) != 0;
+            if (!ok) break;
+            if (valid) {
+                const TcProblem &p = a.p[it.pi];
+                float *tab = tabs + (i & 1) * M::kTab;
+                const float g = fmaxf(__ldg(a.log_decay + it.h), -1e30f);  // -inf: 0 * -inf must be 0
+                for (int k = lane; k <= kC; k += 32) tab[M::kPw + k] = expf((float)k * g);
+                const float w = p.ps * expf((float)lane * g);
+                tab[M::kDiag + 31 + lane] = p.rev && lane > 0 ? 0.0f : w;
+                if (lane > 0) tab[M::kDiag + 31 - lane] = p.rev ? w : 0.0f;
+                tab[M::kCf + (p.rev ? lane : 31 - lane)] = expf((float)lane * g);
+            }
+            if (lane == 0) items[i & 1] = it;
+            __syncwarp();
+            if (lane == 0) bar_arrive(bar(kBarItem + (i & 1)));
+            if (!valid) break;
+            if (lane == 0) {
+                const TcProblem &p = a.p[it.pi];
+                const CUtensorMap *mx = &maps.m[p.mx], *my = &maps.m[p.my], *mz = &maps.m[p.mz];
+                const int b = a.seq_start ? 0 : it.seq, z0 = kZ * it.zb, dt = p.rev ? -kC : kC;
+                const int hx = it.h / p.xg, hy = it.h / p.yg, hz = it.h / p.zg;
+                int t = it.row0;
+#pragma unroll 1
+                for (int c = 0; c < it.nc; ++c, t += dt, ring.next()) {
+                    const int st = ring.st, use = ring.use;
+                    const uint32_t dst = sbase + (uint32_t)(st * M::kStage);
+                    if (use > 0 && !(ok = wait(kBarYFree + st, use - 1))) break;
+                    bar_arrive_tx(bar(kBarY + st), (uint32_t)M::kY);
+#pragma unroll
+                    for (int q = 0; q < DX / 64; ++q) tma_load4(my, dst + M::kX + q * 16384, bar(kBarY + st), 64 * q, hy, t, b);
+                    ++sent[0];
+                    if (use > 0 && !(ok = wait(kBarZFree + st, use - 1))) break;
+                    bar_arrive_tx(bar(kBarZ + st), (uint32_t)M::kZb);
+                    tma_load4(mz, dst + M::kX + M::kY, bar(kBarZ + st), z0, hz, t, b);
+                    ++sent[1];
+                    if constexpr (!kOwn) {
+                        if (use > 0 && !(ok = wait(kBarXFree + st, use - 1))) break;
+                        bar_arrive_tx(bar(kBarX + st), (uint32_t)M::kX);
+#pragma unroll
+                        for (int q = 0; q < DX / 64; ++q) tma_load4(mx, dst + q * 16384, bar(kBarX + st), 64 * q, hx, t, b);
+                        ++sent[2];
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        // when stopping, the copies issued have landed before the CTA ends
+        for (int q = 0; q < 3 && !ok && lane == 0; ++q)
+            for (int i = sent[q] < NS ? 0 : sent[q] - NS; i < sent[q]; ++i)
+                for (uint32_t k = 0;
+                     k < kSpinTries && !bar_try(bar((q == 0 ? kBarY : q == 1 ? kBarZ : kBarX) + i % NS), (uint32_t)(i / NS) & 1u); ++k) {}
+    } else if (warp == R::kQk) {
+        if constexpr (!kOwn) {
+            const uint64_t dx0 = sdesc(sbase, 0), dy0 = sdesc(sbase + M::kX, 0);
+            uint32_t cleared = 0;  // per stage, the parity of its cleared chunks
+            each_item([&](const Item &it, const float *) {
+                const int nc = it.nc, cpart = it.cpart;
+#pragma unroll 1
+                for (int c = 0; c < nc; ++c, ++cc, ring.next()) {
+                    const int b = cc & 1, st = ring.st;
+                    if (!wait_all(kBarX + st, ring.use) || !wait_all(kBarY + st, ring.use)) return false;
+                    if (c == cpart) {
+                        if (!wait_all(kBarClear + st, (int)(cleared >> st) & 1)) return false;
+                        cleared ^= 1u << st;
+                    }
+                    if (cc >= 2 && !wait_all(kBarOFree + b, (cc - 2) >> 1)) return false;
+                    tc_after();
+                    if (elect_one()) {
+                        const uint64_t x = dstep(dx0, st * M::kStage), y = dstep(dy0, st * M::kStage);
+#pragma unroll
+                        for (int k = 0; k < KX; ++k) {
+                            const uint32_t off = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32);
+                            mma(tmem + col_qk(b), dstep(x, off), dstep(y, off), idesc(kC, false, false), k > 0);
+                        }
+                        mma_commit(bar(kBarQK + b));
+                        mma_commit(bar(kBarXFree + st));
+                        mma_commit(bar(kBarYFree + st));
+                    }
+                    __syncwarp();
+                }
+                return true;
+            });
+            drain(0);
         }
     } else if (warp == R::kKv) {
-        if (lane == 0) {
-            // dx <= 64: the second 64 rows of the product repeat the first
-            const uint64_t dy0 = sdesc(sbase + M::kX, DX == 64 ? 0 : 16384), dz = sdesc(sbase + M::oZs, M::kZb);
-            bool ok = true;
+        // dx <= 64: the second 64 rows of the product repeat the first
+        const uint64_t dy0 = sdesc(sbase + M::kX, DX == 64 ? 0 : 16384), dz = sdesc(sbase + M::oZs, M::kZb);
+        each_item([&](const Item &it, const float *) {
+            const int nc = it.nc;
 #pragma unroll 1
-            for (int c = 0; c < nc && ok; ++c, ring.next()) {
+            for (int c = 0; c < nc; ++c, ++cc, ring.next()) {
                 const int st = ring.st;
-                const uint64_t y = dstep(dy0, st * M::kStage);
-                if (!(ok = wait(kBarY + st, ring.use)) || (c > 0 && !(ok = wait(kBarKVFree, c - 1)))) break;
+                if (!wait_all(kBarY + st, ring.use) || (cc > 0 && !wait_all(kBarKVFree, cc - 1))) return false;
 #pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf) {
-                    if (!(ok = wait(kBarZs + hf, c))) break;
+                    if (!wait_all(kBarZs + hf, cc)) return false;
                     tc_after();
+                    if (elect_one()) {
+                        const uint64_t y = dstep(dy0, st * M::kStage + 8192 * hf), z = dstep(dz, 8192 * hf);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma(tmem + kColKv, dstep(y, 8192 * hf + 2048 * k), dstep(dz, 8192 * hf + 2048 * k),
-                            idesc(3 * kZ, true, true), hf > 0 || k > 0);
-                    mma_commit(bar(kBarZsFree + hf));
+                        for (int k = 0; k < 4; ++k)
+                            mma(tmem + kColKv, dstep(y, 2048 * k), dstep(z, 2048 * k), idesc(3 * kZ, true, true), hf > 0 || k > 0);
+                        mma_commit(bar(kBarZsFree + hf));
+                        if (hf == 1) {
+                            mma_commit(bar(kBarKV));
+                            mma_commit(bar(kBarYFree + st));
+                        }
+                    }
+                    __syncwarp();
                 }
-                mma_commit(bar(kBarKV));
-                mma_commit(bar(kBarYFree + st));
             }
-            drain(1);
-        }
+            return true;
+        });
+        drain(1);
     } else if (warp == R::kO) {
-        if constexpr (!kStates) {
-            if (lane == 0) {
-                const uint64_t dx0 = sdesc(sbase, 0), dz0 = sdesc(sbase + M::kX + M::kY, 0), ds = sdesc(sbase + M::oS, 0);
+        if constexpr (!kOwn) {
+            const uint64_t dx0 = sdesc(sbase, 0), dz0 = sdesc(sbase + M::kX + M::kY, 0), ds = sdesc(sbase + M::oS, 0);
+            each_item([&](const Item &it, const float *) {
+                const int nc = it.nc;
 #pragma unroll 1
-                for (int c = 0; c < nc; ++c, ring.next()) {
-                    const int b = c & 1, st = ring.st;
-                    if (!wait(kBarX + st, ring.use) || !wait(kBarZ + st, ring.use) || !wait(kBarS, c) ||
-                        (c > 0 && !wait(kBarOFree + (b ^ 1), (c - 1) >> 1)))
-                        break;
+                for (int c = 0; c < nc; ++c, ++cc, ring.next()) {
+                    const int b = cc & 1, st = ring.st;
+                    if (!wait_all(kBarX + st, ring.use) || !wait_all(kBarZ + st, ring.use) || !wait_all(kBarS, cc) ||
+                        (cc > 0 && !wait_all(kBarOFree + (b ^ 1), (cc - 1) >> 1)))
+                        return false;
                     tc_after();
-                    const uint64_t x = dstep(dx0, st * M::kStage), z = dstep(dz0, st * M::kStage);
+                    if (elect_one()) {
+                        const uint64_t x = dstep(dx0, st * M::kStage);
 #pragma unroll
-                    for (int k = 0; k < KX; ++k)
-                        mma(tmem + kColOb, dstep(x, (k >> 2) * 16384 + (k & 3) * 32), dstep(ds, 2048 * k),
-                            idesc(kZ, false, true), k > 0);
-                    mma_commit(bar(kBarOB));
-                    mma_commit(bar(kBarXFree + st));
-                    if (!wait(kBarP + b, c >> 1)) break;
+                        for (int k = 0; k < KX; ++k)
+                            mma(tmem + kColOb, dstep(x, (k >> 2) * 16384 + (k & 3) * 32), dstep(ds, 2048 * k),
+                                idesc(kZ, false, true), k > 0);
+                        mma_commit(bar(kBarOB));
+                        mma_commit(bar(kBarXFree + st));
+                    }
+                    __syncwarp();
+                    if (!wait_all(kBarP + b, cc >> 1)) return false;
                     tc_after();
+                    if (elect_one()) {
+                        const uint64_t z = dstep(dz0, st * M::kStage);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ts(tmem + col_oa(b), tmem + col_qk(b) + 8u * k, dstep(z, 2048 * k), idesc(kZ, false, true), k > 0);
-                    mma_commit(bar(kBarO + b));
+                        for (int k = 0; k < 8; ++k)
+                            mma_ts(tmem + col_oa(b), tmem + col_qk(b) + 8u * k, dstep(z, 2048 * k), idesc(kZ, false, true), k > 0);
+                        mma_commit(bar(kBarO + b));
+                    }
+                    __syncwarp();
                 }
-                drain(2);
-            }
+                return true;
+            });
+            drain(2);
         }
     } else if (warp < 4) {
         // ================================= group P =================================
-        if constexpr (!kStates) {
+        if constexpr (!kOwn) {
             const int t = 32 * warp + lane;
             const uint32_t lanes = tmem + ((uint32_t)(32 * warp) << 16);
-            // a block of 32 columns before the diagonal: lam^|t - s| from the row's distance to the
-            // block's edge (rf, a step per block) and the column's (cf); the block on the diagonal
-            // from a table by t - s, one side of which is zeros; behind it, zeros
-            const float *cf = reinterpret_cast<const float *>(smem + M::oCf);
-            const float *dg = reinterpret_cast<const float *>(smem + M::oDiag) + 31 + lane;
-            const float *rf0 = reinterpret_cast<const float *>(smem + M::oPs) + (rev ? -t : t - 31);
-            const int past0 = rev ? -warp : warp, dpast = rev ? 1 : -1, drf = rev ? 32 : -32;
+            each_item([&](const Item &it, const float *tab) {
+                // a block of 32 columns before the diagonal: lam^|t - s| from the row's distance to the
+                // block's edge (rf, a step per block) and the column's (cf); the block on the diagonal
+                // from a table by t - s, one side of which is zeros; behind it, zeros
+                const TcProblem &p = a.p[it.pi];
+                const bool rev = p.rev != 0;
+                const float ps = p.ps;
+                const float *cf = tab + M::kCf, *dg = tab + M::kDiag + 31 + lane, *rf0 = tab + M::kPw + (rev ? -t : t - 31);
+                const int past0 = rev ? -warp : warp, dpast = rev ? 1 : -1, drf = rev ? 32 : -32, nc = it.nc;
 #pragma unroll 1
-            for (int c = 0; c < nc; ++c) {
-                const uint32_t qk = lanes + col_qk(c & 1);
-                if (!wait_all(kBarQK + (c & 1), c >> 1)) break;
-                tc_after();
-                int past = past0;  // blocks between this one and the diagonal
-                const float *rf = rf0;
+                for (int c = 0; c < nc; ++c, ++cc) {
+                    const uint32_t qk = lanes + col_qk(cc & 1);
+                    if (!wait_all(kBarQK + (cc & 1), cc >> 1)) return false;
+                    tc_after();
+                    int past = past0;  // blocks between this one and the diagonal
+                    const float *rf = rf0;
 #pragma unroll 1
-                for (int jb = 0; jb < 4; ++jb, past += dpast, rf += drf) {
-                    uint32_t r[16];
-                    if (past < 0) {
+                    for (int jb = 0; jb < 4; ++jb, past += dpast, rf += drf) {
+                        uint32_t r[16];
+                        if (past < 0) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = 0u;
-                    } else {
-                        float v[32];
-                        tmem_ld32(qk + 32u * jb, v);
-                        if (past > 0) {
-                            const f2 w = f2_splat(*rf);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                f2 w0, w1;
-                                lds_f2x2(cf + i, w0, w1);
-                                r[i / 2] = pack2(f2_mul(f2_make(v[i], v[i + 1]), f2_mul(w, w0)));
-                                r[i / 2 + 1] = pack2(f2_mul(f2_make(v[i + 2], v[i + 3]), f2_mul(w, w1)));
-                            }
+                            for (int i = 0; i < 16; ++i) r[i] = 0u;
                         } else {
+                            float v[32];
+                            tmem_ld32(qk + 32u * jb, v);
+                            if (past > 0) {
+                                const f2 w = f2_splat(ps * *rf);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) r[i / 2] = pack2(v[i] * dg[-i], v[i + 1] * dg[-i - 1]);
+                                for (int i = 0; i < 32; i += 4) {
+                                    f2 w0, w1;
+                                    lds_f2x2(cf + i, w0, w1);
+                                    r[i / 2] = pack2(f2_mul(f2_make(v[i], v[i + 1]), f2_mul(w, w0)));
+                                    r[i / 2 + 1] = pack2(f2_mul(f2_make(v[i + 2], v[i + 3]), f2_mul(w, w1)));
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 32; i += 2) r[i / 2] = pack2(v[i] * dg[-i], v[i + 1] * dg[-i - 1]);
+                            }
                         }
+                        tmem_st16(qk + 16u * jb, r);
                     }
-                    tmem_st16(qk + 16u * jb, r);
+                    tmem_st_wait();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(kBarP + (cc & 1)));
                 }
-                tmem_st_wait();
-                tc_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(bar(kBarP + (c & 1)));
-            }
+                return true;
+            });
         }
     } else if (warp >= R::kE0) {
         // ================================= group E =================================
-        if constexpr (!kStates) {
-            const int t = 32 * (warp - R::kE0) + lane;
-            const uint32_t lanes = tmem + ((uint32_t)(32 * (warp - R::kE0)) << 16);
-            const int cols = p.dz - kZ * zb < kZ ? p.dz - kZ * zb : kZ;
-            const int64_t at = (a.seq_start ? 0 : (int64_t)pl.seq * p.o_sb) + (int64_t)h * p.o_sh + kZ * zb +
-                               (int64_t)(row0 + 32 * (warp - R::kE0) + (lane >> 3)) * p.o_sl;
-            const int es = p.o_f32 ? 4 : 2;
+        if constexpr (!kOwn) {
+            const int t0 = 32 * (warp - R::kE0), t = t0 + lane;
+            const uint32_t lanes = tmem + ((uint32_t)t0 << 16);
             // A thread holds a row, but stores that touch 32 rows at once keep the load-store unit
             // from everybody else (2000 clocks a chunk): rows go through the chunk's Z tile, which
             // nothing reads any more, and leave 128 bytes of 4 rows at a time.
             const int q = lane & 7, r4 = lane >> 3;
-            unsigned char *o = static_cast<unsigned char *>(p.o) + at * es + 16 * q;
-            const int64_t step = (int64_t)dt * p.o_sl * es, row4 = 4 * p.o_sl * es;
-            const float *te = reinterpret_cast<const float *>(smem + M::oTe) + t;
             const uint32_t zrow = (uint32_t)(M::kX + M::kY) + 128u * t;
-            const uint32_t zcol = (uint32_t)(M::kX + M::kY) + 128u * (32 * (warp - R::kE0) + r4);
+            const uint32_t zcol = (uint32_t)(M::kX + M::kY) + 128u * (t0 + r4);
+            each_item([&](const Item &it, const float *tab) {
+                const TcProblem &p = a.p[it.pi];
+                const bool rev = p.rev != 0;
+                const int nc = it.nc, cpart = it.cpart, npart = it.npart, es = p.o_f32 ? 4 : 2;
+                const int bytes = (p.dz - kZ * it.zb < kZ ? p.dz - kZ * it.zb : kZ) * es;  // of a row
+                const int64_t at = (a.seq_start ? 0 : (int64_t)it.seq * p.o_sb) + (int64_t)it.h * p.o_sh + kZ * it.zb +
+                                   (int64_t)(it.row0 + t0 + r4) * p.o_sl;
+                unsigned char *o = static_cast<unsigned char *>(p.o) + at * es + 16 * q;
+                const int64_t step = (int64_t)(rev ? -kC : kC) * p.o_sl * es, row4 = 4 * p.o_sl * es;
+                const float ro = p.ro, *pw = tab + M::kPw;
 #pragma unroll 1
-            for (int c = 0; c < nc; ++c, o += step, ring.next()) {
-                const int b = c & 1, n = c == cpart ? npart : kC, nw = n - 32 * (warp - R::kE0) - r4;
-                const f2 rf = f2_splat(t < n ? te[rev ? kC - n : 0] : 0.0f);
-                const uint32_t oa = lanes + col_oa(b), ob = lanes + kColOb;
-                const uint32_t tile = sbase + (uint32_t)(ring.st * M::kStage);
-                // 128 bytes of every row from the tile to o, `off` bytes into the row; the tile is
-                // free as soon as it is read
-                auto copy_out = [&](int off, bool last) {
-                    __syncwarp();
-                    uint4 v[8];
+                for (int c = 0; c < nc; ++c, ++cc, o += step, ring.next()) {
+                    const int b = cc & 1, n = c == cpart ? npart : kC, nw = n - t0 - r4;
+                    const f2 rf = f2_splat(t < n ? ro * pw[rev ? n - 1 - t : t + 1] : 0.0f);
+                    const uint32_t oa = lanes + col_oa(b), ob = lanes + kColOb;
+                    const uint32_t tile = sbase + (uint32_t)(ring.st * M::kStage);
+                    // 128 bytes of every row from the tile to o, `off` bytes into the row; the tile is
+                    // free as soon as it is read
+                    auto copy_out = [&](int off, bool last) {
+                        __syncwarp();
+                        uint4 v[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = lds128(tile + zcol + 512u * i + (uint32_t)((q ^ ((4 * i + r4) & 7)) << 4));
-                    if (last) fence_async_smem();  // (its next use is a copy's)
-                    __syncwarp();
-                    if (last && lane == 0) bar_arrive(bar(kBarZFree + ring.st));
+                        for (int i = 0; i < 8; ++i) v[i] = lds128(tile + zcol + 512u * i + (uint32_t)((q ^ ((4 * i + r4) & 7)) << 4));
+                        if (last) fence_async_smem();  // (its next use is a copy's)
+                        __syncwarp();
+                        if (last && lane == 0) bar_arrive(bar(kBarZFree + ring.st));
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (4 * i < nw && off + 16 * q < cols * es) *reinterpret_cast<uint4 *>(o + off + i * row4) = v[i];
-                };
-                if (!wait_all(kBarO + b, c >> 1)) break;
-                tc_after();
-                if (es == 2) {
-                    uint32_t r[kZ / 2];
+                        for (int i = 0; i < 8; ++i)
+                            if (4 * i < nw && off + 16 * q < bytes) *reinterpret_cast<uint4 *>(o + off + i * row4) = v[i];
+                    };
+                    if (!wait_all(kBarO + b, cc >> 1)) return false;
+                    tc_after();
+                    if (es == 2) {
+                        uint32_t r[kZ / 2];
 #pragma unroll
-                    for (int i = 0; i < kZ; i += 16) {
-                        float v[16], w[16];
-                        tmem_ld2x16(oa + (uint32_t)i, ob + (uint32_t)i, v, w);
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2)
-                            r[(i + j) >> 1] = pack2(f2_fma(rf, f2_make(w[j], w[j + 1]), f2_make(v[j], v[j + 1])));
-                    }
-                    tc_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(bar(kBarOFree + b));
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        sts128(tile + zrow + (uint32_t)((i ^ (t & 7)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-                    copy_out(0, true);
-                } else {
-#pragma unroll 1
-                    for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 16) {
+                        for (int i = 0; i < kZ; i += 16) {
                             float v[16], w[16];
-                            tmem_ld2x16(oa + (uint32_t)(32 * hf + i), ob + (uint32_t)(32 * hf + i), v, w);
+                            tmem_ld2x16(oa + (uint32_t)i, ob + (uint32_t)i, v, w);
 #pragma unroll
                             for (int j = 0; j < 16; j += 2)
-                                f2_split(f2_fma(rf, f2_make(w[j], w[j + 1]), f2_make(v[j], v[j + 1])), v[j], v[j + 1]);
+                                r[(i + j) >> 1] = pack2(f2_fma(rf, f2_make(w[j], w[j + 1]), f2_make(v[j], v[j + 1])));
+                        }
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(bar(kBarOFree + b));
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4)
-                                sts128(tile + zrow + (uint32_t)((((i + j) >> 2) ^ (t & 7)) << 4), __float_as_uint(v[j]),
-                                       __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3]));
+                        for (int i = 0; i < 8; ++i)
+                            sts128(tile + zrow + (uint32_t)((i ^ (t & 7)) << 4), r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                        copy_out(0, true);
+                    } else {
+#pragma unroll 1
+                        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 16) {
+                                float v[16], w[16];
+                                tmem_ld2x16(oa + (uint32_t)(32 * hf + i), ob + (uint32_t)(32 * hf + i), v, w);
+#pragma unroll
+                                for (int j = 0; j < 16; j += 2)
+                                    f2_split(f2_fma(rf, f2_make(w[j], w[j + 1]), f2_make(v[j], v[j + 1])), v[j], v[j + 1]);
+#pragma unroll
+                                for (int j = 0; j < 16; j += 4)
+                                    sts128(tile + zrow + (uint32_t)((((i + j) >> 2) ^ (t & 7)) << 4), __float_as_uint(v[j]),
+                                           __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]), __float_as_uint(v[j + 3]));
+                            }
+                            if (hf == 1) {
+                                tc_before();
+                                __syncwarp();
+                                if (lane == 0) bar_arrive(bar(kBarOFree + b));
+                            }
+                            copy_out(128 * hf, hf == 1);
                         }
-                        if (hf == 1) {
-                            tc_before();
-                            __syncwarp();
-                            if (lane == 0) bar_arrive(bar(kBarOFree + b));
-                        }
-                        copy_out(128 * hf, hf == 1);
                     }
                 }
-            }
+                return true;
+            });
         }
     } else if (warp < R::kS0) {
         // ================================= group V =================================
-        constexpr int VT = 32 * R::kV, kItems = kC * 8 / VT / 2;  // 16-byte items a thread has in each half
+        constexpr int VT = 32 * R::kV, kItems = kC * 8 / VT / 2;  // 16-byte pieces a thread has in each half
         const int gt = tid - 32 * R::kV0;
         const uint32_t zs = sbase + M::oZs + 16u * gt;
-        const float *tv0 = reinterpret_cast<const float *>(smem + M::oTv) + (gt >> 3);
-        bool ok = true;
+        each_item([&](const Item &it, const float *tab) {
+            const TcProblem &p = a.p[it.pi];
+            const bool rev = p.rev != 0;
+            const int nc = it.nc, cpart = it.cpart, npart = it.npart, dpw = rev ? VT / 8 : -VT / 8;
+            const float ws = p.ws;
 #pragma unroll 1
-        for (int c = 0; c < nc && ok; ++c, ring.next()) {
-            const int st = ring.st, n = c == cpart ? npart : kC;
-            const uint32_t y = sbase + (uint32_t)(st * M::kStage + M::kX), z = y + M::kY + 16u * gt;
-            if (!wait_all(kBarZ + st, ring.use)) break;
-            if (n < kC) {
-                // the rows behind the sequence, before any product reads them
-                if (!wait_all(kBarY + st, ring.use)) break;
+            for (int c = 0; c < nc; ++c, ++cc, ring.next()) {
+                const int st = ring.st, n = c == cpart ? npart : kC;
+                const uint32_t y = sbase + (uint32_t)(st * M::kStage + M::kX), z = y + M::kY + 16u * gt;
+                if (!wait_all(kBarZ + st, ring.use)) return false;
+                if (n < kC) {
+                    // the rows behind the sequence, before any product reads them
+                    if (!wait_all(kBarY + st, ring.use)) return false;
 #pragma unroll 1
-                for (int i = n * 8 + gt; i < kC * 8; i += VT) {
-                    sts128(y + M::kY + 16 * i, 0, 0, 0, 0);
+                    for (int i = n * 8 + gt; i < kC * 8; i += VT) {
+                        sts128(y + M::kY + 16 * i, 0, 0, 0, 0);
 #pragma unroll
-                    for (int j = 0; j < DX / 64; ++j) sts128(y + j * 16384 + 16 * i, 0, 0, 0, 0);
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) bar_arrive(bar(kBarClear));
-            }
-            const float *tv = tv0 + (rev ? 0 : kC - n);
-#pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {
-                if (c > 0 && !(ok = wait_all(kBarZsFree + hf, c - 1))) break;
-#pragma unroll 1
-                for (int it = kItems * hf; it < kItems * (hf + 1); ++it) {
-                    // 8 columns of row VT / 8 it + gt / 8
-                    uint4 q = make_uint4(0, 0, 0, 0), hi, mid, lo;
-                    float w = 0.0f;
-                    if (VT / 8 * it + (gt >> 3) < n) {
-                        w = tv[VT / 8 * it];
-                        q = lds128(z + 16u * VT * it);
+                        for (int j = 0; j < DX / 64; ++j) sts128(y + j * 16384 + 16 * i, 0, 0, 0, 0);
                     }
-                    const f2 w2 = f2_splat(w);
-                    split3(w2, q.x, hi.x, mid.x, lo.x);
-                    split3(w2, q.y, hi.y, mid.y, lo.y);
-                    split3(w2, q.z, hi.z, mid.z, lo.z);
-                    split3(w2, q.w, hi.w, mid.w, lo.w);
-                    sts128(zs + 16u * VT * it, hi.x, hi.y, hi.z, hi.w);
-                    sts128(zs + 16u * VT * it + M::kZb, mid.x, mid.y, mid.z, mid.w);
-                    sts128(zs + 16u * VT * it + 2 * M::kZb, lo.x, lo.y, lo.z, lo.w);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(kBarClear + st));
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(bar(kBarZs + hf));
-                    if (hf == 1) bar_arrive(bar(kBarZFree + st));
+                // the weight of row gt / 8 + VT / 8 k
+                const float *pw = tab + M::kPw + (rev ? (gt >> 3) + 1 : n - 1 - (gt >> 3));
+#pragma unroll 1
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (cc > 0 && !wait_all(kBarZsFree + hf, cc - 1)) return false;
+#pragma unroll 1
+                    for (int k = kItems * hf; k < kItems * (hf + 1); ++k) {
+                        uint4 q = make_uint4(0, 0, 0, 0), hi, mid, lo;
+                        float w = 0.0f;
+                        if (VT / 8 * k + (gt >> 3) < n) {
+                            w = ws * pw[dpw * k];
+                            q = lds128(z + 16u * VT * k);
+                        }
+                        const f2 w2 = f2_splat(w);
+                        split3(w2, q.x, hi.x, mid.x, lo.x);
+                        split3(w2, q.y, hi.y, mid.y, lo.y);
+                        split3(w2, q.z, hi.z, mid.z, lo.z);
+                        split3(w2, q.w, hi.w, mid.w, lo.w);
+                        sts128(zs + 16u * VT * k, hi.x, hi.y, hi.z, hi.w);
+                        sts128(zs + 16u * VT * k + M::kZb, mid.x, mid.y, mid.z, mid.w);
+                        sts128(zs + 16u * VT * k + 2 * M::kZb, lo.x, lo.y, lo.z, lo.w);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(bar(kBarZs + hf));
+                        if (hf == 1) bar_arrive(bar(kBarZFree + st));
+                    }
                 }
             }
-        }
+            return true;
+        });
     } else {
         // ================================= group S =================================
         // dx <= 64: KV's second 64 rows repeat the first, so warps 2 and 3 take the
@@ -737,79 +881,115 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
         constexpr int NCOL = DX == 64 ? 32 : 64;
         const int w = warp - R::kS0, row = (DX == 64 ? 32 * (w & 1) : 32 * w) + lane, c0 = DX == 64 ? 32 * (w >> 1) : 0;
         const uint32_t kv = tmem + ((uint32_t)(32 * w) << 16) + kColKv + (uint32_t)c0;
-        f2 S[NCOL / 2];
-        const int64_t blk = p.dx * (int64_t)p.dz;
-        {
-            const int64_t hb = (int64_t)h * blk, sb = a.H * blk;
-            auto add = [&](const float *from, int64_t sr, int64_t sc, float decay) {
-                const bool in = from && row < p.dx;
-                const int64_t at = row * sr + (kZ * zb + c0) * sc;
-#pragma unroll
-                for (int i = 0; i < NCOL; i += 2) {
-                    const bool use = in && kZ * zb + c0 + i < p.dz;  // (dz is a multiple of 8)
-                    const float u = use ? from[at + i * sc] : 0.0f, v = use ? from[at + (i + 1) * sc] : 0.0f;
-                    S[i / 2] = f2_fma(f2_splat(decay), S[i / 2], f2_make(u, v));
-                }
-            };
-#pragma unroll
-            for (int i = 0; i < NCOL / 2; ++i) S[i] = f2_splat(0.0f);
-            if constexpr (!kStates) {
-                add(p.s0 ? p.s0 + pl.seq * sb + hb : nullptr, p.s0_sr, p.s0_sc, 0.0f);
-                // the earlier segments' own states, in the order of work
-                if (p.seg_states)
-#pragma unroll 1
-                    for (int j = rev ? pl.ng - 1 : 0; j != pl.g; j += rev ? -1 : 1) {
-                        const int n = pl.len - j * a.seg < a.seg ? pl.len - j * a.seg : a.seg;
-                        add(p.seg_states + (int64_t)(slot - pl.g + j) * sb + hb, p.seg_sr, p.seg_sc, expf((float)n * g));
-                    }
-            }
-        }
-        // lam^n S as keep S + part S, rounded once: with lam^n >= 1/2 part = lam^n - 1 keeps the
-        // bits of a slow decay over many chunks
-        const float m = expm1f((float)kC * g), mp = expm1f((float)npart * g);
-        const float keep = m >= -0.5f ? 1.0f : 0.0f, part = m >= -0.5f ? m : expf((float)kC * g);
-        const float keepp = mp >= -0.5f ? 1.0f : 0.0f, partp = mp >= -0.5f ? mp : expf((float)npart * g);
         const uint32_t dst = sbase + M::oS + 128u * row;
         const int x8 = row & 7, j0 = c0 >> 3;
-        bool ok = true;
+        each_item([&](const Item &it, const float *tab) {
+            const TcProblem &p = a.p[it.pi];
+            const bool rev = p.rev != 0;
+            const int nc = it.nc, cpart = it.cpart, col0 = kZ * it.zb + c0;
+            const int64_t blk = p.dx * (int64_t)p.dz, hb = (int64_t)it.h * blk, sb = a.H * blk;
+            const float g = fmaxf(__ldg(a.log_decay + it.h), -1e30f);
+            const int chain = (it.seq * a.H + it.h) * a.units + it.unit;
+            f2 S[NCOL / 2];
+#pragma unroll
+            for (int i = 0; i < NCOL / 2; ++i) S[i] = f2_splat(0.0f);
+            if constexpr (!kOwn) {
+                // decay * S + an array's block
+                auto add = [&](const float *from, int64_t sr, int64_t sc, float decay) {
+                    const bool in = from && row < p.dx;
+                    const int64_t at = row * sr + col0 * sc;
+#pragma unroll
+                    for (int i = 0; i < NCOL; i += 2) {
+                        const bool use = in && col0 + i < p.dz;  // (dz is a multiple of 8)
+                        const float u = use ? from[at + i * sc] : 0.0f, v = use ? from[at + (i + 1) * sc] : 0.0f;
+                        S[i / 2] = f2_fma(f2_splat(decay), S[i / 2], f2_make(u, v));
+                    }
+                };
+                if (kMode == kChained && it.j > 0) {
+                    // from the previous segment's item, once its four warps have handed it on
+                    bool there = true;
+                    if (lane == 0) {
+                        there = false;
+                        for (uint32_t k = 0; k < kFlagTries && !there; ++k) {
+                            there = ld_acquire(a.flags + chain) >= 4 * it.j;
+                            if (!there && (k & 63u) == 63u && *abort_flag != 0u) break;
+                        }
+                        if (!there) {
+                            if (a.status && *abort_flag == 0u) atomicOr(a.status, MS_ERR_TIMEOUT);
+                            *abort_flag = 1u;
+                        }
+                    }
+                    if (!__shfl_sync(0xffffffffu, there, 0)) return false;
+                    const float4 *from = reinterpret_cast<const float4 *>(a.chain + ((int64_t)chain * DX + row) * kZ + c0);
+#pragma unroll
+                    for (int i = 0; i < NCOL; i += 4) {
+                        const float4 v = __ldcg(from + i / 4);
+                        S[i / 2] = f2_make(v.x, v.y);
+                        S[i / 2 + 1] = f2_make(v.z, v.w);
+                    }
+                } else {
+                    add(p.s0 ? p.s0 + it.seq * sb + hb : nullptr, p.s0_sr, p.s0_sc, 0.0f);
+                    // the earlier segments' own states, in the order of work
+                    if (kMode == kStates)
 #pragma unroll 1
-        for (int c = 0; c < nc; ++c) {
-            if constexpr (!kStates) {
-                if (c > 0 && !(ok = wait_all(kBarOB, c - 1))) break;
+                        for (int j = 0; j < it.j; ++j) {
+                            const int s = rev ? it.ng - 1 - j : j, n = it.len - s * a.seg < a.seg ? it.len - s * a.seg : a.seg;
+                            add(p.seg_states + (int64_t)(it.slot0 + s) * sb + hb, p.seg_sr, p.seg_sc, expf((float)n * g));
+                        }
+                }
+            }
+            // lam^n S as keep S + part S, rounded once: with lam^n >= 1/2 part = lam^n - 1 keeps the
+            // bits of a slow decay over many chunks
+            const float m = expm1f((float)kC * g), mp = expm1f((float)it.npart * g);
+            const float keep = m >= -0.5f ? 1.0f : 0.0f, part = m >= -0.5f ? m : tab[M::kPw + kC];
+            const float keepp = mp >= -0.5f ? 1.0f : 0.0f, partp = mp >= -0.5f ? mp : tab[M::kPw + it.npart];
+#pragma unroll 1
+            for (int c = 0; c < nc; ++c, ++cc) {
+                if constexpr (!kOwn) {
+                    if (cc > 0 && !wait_all(kBarOB, cc - 1)) return false;
 #pragma unroll
-                for (int i = 0; i < NCOL; i += 8)
-                    sts128(dst + (uint32_t)(((j0 + (i >> 3)) ^ x8) << 4), pack2(S[i / 2]), pack2(S[i / 2 + 1]),
-                           pack2(S[i / 2 + 2]), pack2(S[i / 2 + 3]));
-                fence_async_smem();
+                    for (int i = 0; i < NCOL; i += 8)
+                        sts128(dst + (uint32_t)(((j0 + (i >> 3)) ^ x8) << 4), pack2(S[i / 2]), pack2(S[i / 2 + 1]),
+                               pack2(S[i / 2 + 2]), pack2(S[i / 2 + 3]));
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(bar(kBarS));
+                }
+                // lam^n S while KV is formed (before the wait: KV's columns are needed for the next chunk)
+                const f2 k2 = f2_splat(c == cpart ? keepp : keep), p2 = f2_splat(c == cpart ? partp : part);
+#pragma unroll
+                for (int i = 0; i < NCOL / 2; ++i) S[i] = f2_fma(p2, S[i], f2_mul(k2, S[i]));
+                if (!wait_all(kBarKV, cc)) return false;
+                tc_after();
+#pragma unroll
+                for (int i = 0; i < NCOL; i += 8) {
+                    float hi[8], mid[8], lo[8];
+                    tmem_ld3x8(kv + i, kv + kZ + i, kv + 2 * kZ + i, hi, mid, lo);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2)
+                        S[(i + j) / 2] = f2_add(S[(i + j) / 2], f2_add(f2_make(hi[j], hi[j + 1]),
+                                                                       f2_add(f2_make(mid[j], mid[j + 1]), f2_make(lo[j], lo[j + 1]))));
+                }
+                tc_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(kBarS));
+                if (lane == 0) bar_arrive(bar(kBarKVFree));
             }
-            // lam^n S while KV is formed (before the wait: KV's columns are needed for the next chunk)
-            const f2 k2 = f2_splat(c == cpart ? keepp : keep), p2 = f2_splat(c == cpart ? partp : part);
+            if (kMode == kChained && !kOwn && !it.last) {
+                float4 *to = reinterpret_cast<float4 *>(a.chain + ((int64_t)chain * DX + row) * kZ + c0);
 #pragma unroll
-            for (int i = 0; i < NCOL / 2; ++i) S[i] = f2_fma(p2, S[i], f2_mul(k2, S[i]));
-            if (!(ok = wait_all(kBarKV, c))) break;
-            tc_after();
+                for (int i = 0; i < NCOL; i += 4) *reinterpret_cast<ulonglong2 *>(to + i / 4) = make_ulonglong2(S[i / 2], S[i / 2 + 1]);
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) atomicAdd(a.flags + chain, 1);
+            } else if (p.fin && (kOwn || it.last) && row < p.dx) {
+                const int64_t to = kOwn ? it.slot0 + (rev ? it.ng - 1 - it.j : it.j) : it.seq;
+                float *f = p.fin + to * sb + hb + row * (int64_t)p.dz + col0;
 #pragma unroll
-            for (int i = 0; i < NCOL; i += 8) {
-                float hi[8], mid[8], lo[8];
-                tmem_ld3x8(kv + i, kv + kZ + i, kv + 2 * kZ + i, hi, mid, lo);
-#pragma unroll
-                for (int j = 0; j < 8; j += 2)
-                    S[(i + j) / 2] = f2_add(S[(i + j) / 2], f2_add(f2_make(hi[j], hi[j + 1]),
-                                                                   f2_add(f2_make(mid[j], mid[j + 1]), f2_make(lo[j], lo[j + 1]))));
+                for (int i = 0; i < NCOL; i += 4)
+                    if (col0 + i < p.dz) *reinterpret_cast<ulonglong2 *>(f + i) = make_ulonglong2(S[i / 2], S[i / 2 + 1]);
             }
-            tc_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar(kBarKVFree));
-        }
-        const bool last = rev ? pl.g == 0 : pl.g == pl.ng - 1;
-        if (ok && p.fin && (kStates || last) && row < p.dx) {
-            float *f = p.fin + ((int64_t)(kStates ? slot : pl.seq) * a.H + h) * blk + row * (int64_t)p.dz + kZ * zb + c0;
-#pragma unroll
-            for (int i = 0; i < NCOL; i += 4)
-                if (kZ * zb + c0 + i < p.dz) *reinterpret_cast<ulonglong2 *>(f + i) = make_ulonglong2(S[i / 2], S[i / 2 + 1]);
-        }
+            return true;
+        });
     }
 
     tc_before();
@@ -870,37 +1050,67 @@ MapKey key_z(const LaArgs &a, const LaProblem &p) { return {p.z, p.z_sb, p.z_sl,
 
 int zblocks(int dz) { return (dz + kZ - 1) / kZ; }
 
-// Segments: one block per SM is what runs at a time, so sequences are cut only
-// where sequences, heads and column blocks are fewer than the SMs, into as many
-// segments as fill them once, of at least 512 tokens.
-struct SegPlan {
-    int64_t seg, nseg, slots;
-    bool segmented;
+// How the work is cut (see the top). `chains` runs of chunks over num_sms SMs; a
+// round of items takes as long as their chunks, and half a chunk to change over.
+struct Plan {
+    int mode;
+    int64_t seg, nseg, slots;  // tokens per segment, segments per sequence (dense), slots of segments
 };
-SegPlan seg_plan(int64_t batch, int64_t rows, bool packed, int64_t H, int units, int num_sms) {
-    SegPlan s{};
-    const int64_t base = std::max<int64_t>(1, batch * H * units);
-    const int64_t longest = rows;  // packed: any one of the sequences may have them all
-    const int64_t ways = num_sms / base;
-    s.seg = std::max<int64_t>(512, ((longest + std::max<int64_t>(ways, 1) - 1) / std::max<int64_t>(ways, 1) + kC - 1) / kC * kC);
-    s.segmented = ways >= 2 && s.seg < longest;
-    if (!s.segmented) s.seg = std::max<int64_t>(kC, (longest + kC - 1) / kC * kC + (packed ? kC : 0));
-    s.nseg = s.segmented && !packed ? (rows + s.seg - 1) / s.seg : 1;
-    s.slots = !s.segmented ? batch : packed ? rows / s.seg + batch : batch * s.nseg;
-    return s;
+Plan plan_of(int64_t batch, int64_t rows, bool packed, int64_t H, int units, int num_sms) {
+    const int64_t chains = std::max<int64_t>(1, batch * H * units);
+    // packed: the longest sequence is not known here. kStates goes by the case that one has most rows,
+    // kChained by their mean
+    const int64_t most = (rows + kC - 1) / kC, mean = packed ? (rows / std::max<int64_t>(1, batch) + kC - 1) / kC : most;
+    Plan p{kWhole, 0, 1, batch};
+    int64_t chunks = 0;  // per segment
+    if (2 * chains <= num_sms) {
+        // as many segments as fill the SMs once, twice or three times, of at least four chunks
+        double best = (double)most;
+        for (int r = 1; r <= 3; ++r) {
+            const int64_t n = r * num_sms / chains, len = std::max<int64_t>(4, (most + n - 1) / n);
+            const double t = r * (double)(len + 1) * 1.6;  // the first pass takes 0.6 of the main one
+            if (len < most && t < best) best = t, chunks = len, p.mode = kStates;
+        }
+    } else if (chains > num_sms && mean >= 4) {
+        // equal chains: the segments per chain that leave the least idle at the end
+        auto rounds = [&](int64_t n) { return (n + num_sms - 1) / num_sms; };
+        double best = 0.97 * rounds(chains) * (mean + 0.5);
+        for (int64_t k = 2; 2 * k <= mean; ++k) {
+            const int64_t len = (mean + k - 1) / k;
+            const double t = rounds(chains * k) * (len + 0.5);
+            if (t < best) best = t, chunks = len, p.mode = kChained;
+        }
+    }
+    if (p.mode == kWhole) {
+        p.seg = std::max<int64_t>(1, most + (packed ? 1 : 0)) * kC;
+        return p;
+    }
+    p.seg = chunks * kC;
+    p.nseg = packed ? 1 : (rows + p.seg - 1) / p.seg;
+    p.slots = packed ? rows / p.seg + batch : batch * p.nseg;
+    return p;
 }
+// Workspace: kStates, the segments' states of one direction (forward; and a copy of the
+// initial states, for a call that overwrites them) or two; kChained, ticket and flags, and
+// the chains' states.
+size_t flag_bytes(int64_t chains) { return ((size_t)(chains + 1) * sizeof(int) + 255) / 256 * 256; }
 
-template <int DX, bool kStates>
-cudaError_t launch_t(const TcArgs &a, const TcMaps &maps, int64_t slots, cudaStream_t stream) {
+template <int DX, bool kOwn, int kMode>
+cudaError_t launch_t(const TcArgs &a, const TcMaps &maps, int64_t slots, int num_sms, cudaStream_t stream) {
     static SmemOptIn opt_in;
-    constexpr int bytes = Smem<DX, kStates>::kBytes;
+    constexpr int bytes = Smem<DX, kOwn>::kBytes;
     static_assert(bytes <= 232448, "shared memory of a block");
-    cudaError_t e = opt_in.ensure(reinterpret_cast<const void *>(linattn_tc_kernel<DX, kStates>), bytes);
+    cudaError_t e = opt_in.ensure(reinterpret_cast<const void *>(linattn_tc_kernel<DX, kOwn, kMode>), bytes);
     if (e != cudaSuccess) return e;
-    const int64_t grid = slots * a.H * a.units;
-    if (grid > 0x7fffffffLL || a.seg <= 0) return cudaErrorInvalidConfiguration;
-    linattn_tc_kernel<DX, kStates><<<(unsigned)grid, Roles<DX>::kThreads, bytes, stream>>>(a, maps);
+    const int64_t items = slots * a.H * a.units;
+    if (items > 0x3fffffffLL || a.seg <= 0) return cudaErrorInvalidConfiguration;
+    linattn_tc_kernel<DX, kOwn, kMode><<<(unsigned)std::min<int64_t>(items, num_sms), Roles<DX>::kThreads, bytes, stream>>>(a, maps);
     return cudaGetLastError();
+}
+template <bool kOwn, int kMode>
+cudaError_t launch_dx(int dx, const TcArgs &a, const TcMaps &maps, int64_t slots, int num_sms, cudaStream_t stream) {
+    return dx <= 64 ? launch_t<64, kOwn, kMode>(a, maps, slots, num_sms, stream)
+                    : launch_t<128, kOwn, kMode>(a, maps, slots, num_sms, stream);
 }
 
 }  // namespace
@@ -919,13 +1129,15 @@ bool linattn_tc_applies(const LaArgs &a, bool bf16) {
     return true;
 }
 
-// Bytes of segment states: of one direction (forward), or two (gradients).
 size_t linattn_tc_workspace(int64_t batch, int64_t rows, bool packed, int64_t H, int dk, int dv, bool bwd, int num_sms) {
     if (batch < 1 || rows < 1) return 0;
     const int units = bwd ? 2 * zblocks(dk) + zblocks(dv) : zblocks(dv);
-    const SegPlan s = seg_plan(batch, rows, packed, H, units, num_sms);
-    // (forward: and a copy of the initial states, for a call that overwrites them)
-    return s.segmented ? (size_t)(bwd ? 2 * s.slots : s.slots + batch) * H * dk * dv * sizeof(float) : 0;
+    const Plan p = plan_of(batch, rows, packed, H, units, num_sms);
+    if (p.mode == kStates) return (size_t)(bwd ? 2 * p.slots : p.slots + batch) * H * dk * dv * sizeof(float);
+    if (p.mode == kWhole) return 0;
+    const int64_t chains = batch * H * units;
+    const int dx = (bwd ? std::max(dk, dv) : dk) <= 64 ? 64 : 128;
+    return flag_bytes(chains) + (size_t)chains * dx * kZ * sizeof(float);
 }
 
 cudaError_t launch_linattn_tc(const LaArgs &la, void *workspace, int num_sms, cudaStream_t stream) {
@@ -962,41 +1174,48 @@ cudaError_t launch_linattn_tc(const LaArgs &la, void *workspace, int num_sms, cu
         a.units += t.nzb;
         dxmax = std::max(dxmax, p.dx);
     }
-    const SegPlan sp = seg_plan(la.batch, rows, packed, la.H, a.units, num_sms);
+    const Plan sp = plan_of(la.batch, rows, packed, la.H, a.units, num_sms);
     a.seg = (int)sp.seg;
     a.nseg = (int)sp.nseg;
-    a.segmented = sp.segmented ? 1 : 0;
-    if (sp.segmented) {
-        // the segments' own states: of the forward direction (problem 0), and of the reverse one
-        // (problem 2; problem 1 reads it with rows and columns exchanged, as it does dfinal)
-        TcArgs s = a;
-        float *st = static_cast<float *>(workspace);
-        s.np = la.np == 1 ? 1 : 2;
-        s.units = 0;
-        for (int k = 0; k < s.np; ++k) {
-            const TcProblem &p = a.p[2 * k];
-            s.p[k] = p;
-            s.p[k].fin = st + k * sp.slots * la.H * p.dx * p.dz;
-            s.units += p.nzb;
-        }
-        const cudaError_t e = dxmax <= 64 ? launch_t<64, true>(s, maps, sp.slots, stream)
-                                          : launch_t<128, true>(s, maps, sp.slots, stream);
+    if (sp.mode == kWhole) return launch_dx<false, kWhole>(dxmax, a, maps, sp.slots, num_sms, stream);
+    if (sp.mode == kChained) {
+        const int64_t chains = la.batch * la.H * a.units;
+        const size_t fb = flag_bytes(chains);
+        a.ticket = static_cast<int *>(workspace);
+        a.flags = a.ticket + 1;
+        a.chain = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + fb);
+        const cudaError_t e = cudaMemsetAsync(workspace, 0, fb, stream);
         if (e != cudaSuccess) return e;
-        for (int i = 0; i < la.np; ++i) {
-            a.p[i].seg_states = s.p[i == 0 ? 0 : 1].fin;
-            a.p[i].seg_sr = i == 1 ? 1 : a.p[i].dz;
-            a.p[i].seg_sc = i == 1 ? a.p[i].dx : 1;
-        }
-        if (a.p[0].s0 && a.p[0].s0 == a.p[0].fin) {
-            // a sequence's last segment may end before its others begin
-            const size_t n = (size_t)la.batch * la.H * a.p[0].dx * a.p[0].dz;
-            float *copy = st + (size_t)sp.slots * la.H * a.p[0].dx * a.p[0].dz;
-            const cudaError_t ec = cudaMemcpyAsync(copy, a.p[0].s0, n * sizeof(float), cudaMemcpyDeviceToDevice, stream);
-            if (ec != cudaSuccess) return ec;
-            a.p[0].s0 = copy;
-        }
+        return launch_dx<false, kChained>(dxmax, a, maps, sp.slots, num_sms, stream);
     }
-    return dxmax <= 64 ? launch_t<64, false>(a, maps, sp.slots, stream) : launch_t<128, false>(a, maps, sp.slots, stream);
+    // the segments' own states: of the forward direction (problem 0), and of the reverse one
+    // (problem 2; problem 1 reads it with rows and columns exchanged, as it does dfinal)
+    TcArgs s = a;
+    float *st = static_cast<float *>(workspace);
+    s.np = la.np == 1 ? 1 : 2;
+    s.units = 0;
+    for (int k = 0; k < s.np; ++k) {
+        const TcProblem &p = a.p[2 * k];
+        s.p[k] = p;
+        s.p[k].fin = st + k * sp.slots * la.H * p.dx * p.dz;
+        s.units += p.nzb;
+    }
+    const cudaError_t e = launch_dx<true, kStates>(dxmax, s, maps, sp.slots, num_sms, stream);
+    if (e != cudaSuccess) return e;
+    for (int i = 0; i < la.np; ++i) {
+        a.p[i].seg_states = s.p[i == 0 ? 0 : 1].fin;
+        a.p[i].seg_sr = i == 1 ? 1 : a.p[i].dz;
+        a.p[i].seg_sc = i == 1 ? a.p[i].dx : 1;
+    }
+    if (a.p[0].s0 && a.p[0].s0 == a.p[0].fin) {
+        // a sequence's last segment may end before its others begin
+        const size_t n = (size_t)la.batch * la.H * a.p[0].dx * a.p[0].dz;
+        float *copy = st + (size_t)sp.slots * la.H * a.p[0].dx * a.p[0].dz;
+        const cudaError_t ec = cudaMemcpyAsync(copy, a.p[0].s0, n * sizeof(float), cudaMemcpyDeviceToDevice, stream);
+        if (ec != cudaSuccess) return ec;
+        a.p[0].s0 = copy;
+    }
+    return launch_dx<false, kStates>(dxmax, a, maps, sp.slots, num_sms, stream);
 }
 
 }  // namespace ms
