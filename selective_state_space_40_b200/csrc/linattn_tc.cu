@@ -63,15 +63,9 @@ namespace {
 
 constexpr int kC = 128;   // tokens per chunk
 constexpr int kZ = 64;    // columns of z per CTA
-// The warps of a CTA: group P, group V, group S, group E, and one that loads and
-// three that issue. Group V sets the pace at dx <= 64, so there it has eight warps
-// (NNN); at dx = 128 the registers of S leave room for four.
-template <int DX>
-struct Roles {
-    static constexpr int kV = DX == 64 ? 8 : 4;
-    static constexpr int kV0 = 4, kS0 = kV0 + kV, kE0 = kS0 + 4;
-    static constexpr int kLoad = kE0 + 4, kQk = kLoad + 1, kKv = kLoad + 2, kO = kLoad + 3;
-    static constexpr int kThreads = 32 * (kO + 1);
+// The warps of a CTA: group P, group V, group S, group E (four each), one that loads and three that issue.
+struct R {
+    static constexpr int kV0 = 4, kS0 = 8, kE0 = 12, kLoad = 16, kQk = 17, kKv = 18, kO = 19, kThreads = 640;
 };
 constexpr uint32_t kSpinTries = 1u << 20;   // tries of a barrier
 constexpr uint32_t kFlagTries = 1u << 22;   // polls of a predecessor's flag
@@ -138,13 +132,13 @@ struct Smem {
     static constexpr int oTab = oItem + 2 * (int)sizeof(Item);
     static constexpr int kPw = 0, kDiag = 132, kCf = kDiag + 64, kTab = kCf + 32;  // floats
     static constexpr int oBar = oTab + 2 * kTab * 4;
-    static constexpr int kBytes = oBar + 8 * 46 + 16;
+    static constexpr int kBytes = oBar + 8 * 48 + 16;
 };
 enum {
     kBarX = 0,        // [3] a stage's X, Y, Z tiles are in
     kBarY = 3,
     kBarZ = 6,
-    kBarXFree = 9,    // [3] what uses the stage's X (QK, O_b), Y (QK, KV), Z (groups V, E) is done
+    kBarXFree = 9,    // [3] what uses the stage's X (QK, O_b), Y (QK, KV), Z (group V, O_a, then group E) is done
     kBarYFree = 12,
     kBarZFree = 15,
     kBarQK = 18,      // [2] QK is done
@@ -160,8 +154,9 @@ enum {
     kBarClear = 34,   // [3] the rows behind the sequence are cleared (of a stage's chunk that has some)
     kBarItem = 37,    // [2] an item is laid out
     kBarItemFree = 39,  // [2] every role is done with it
-    kBarEnd = 41,     // [3] nothing of an issuing warp is in flight
-    kNumBars = 44
+    kBarZRead = 41,   // [3] group V has read the stage's Z
+    kBarEnd = 44,     // [3] nothing of an issuing warp is in flight
+    kNumBars = 47
 };
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -321,27 +316,13 @@ __device__ __forceinline__ uint32_t pack2(f2 v) {
     return pack2(a, b);
 }
 __device__ __forceinline__ f2 unpack2(uint32_t v) { return f2_make(bf16_lo(v), bf16_hi(v)); }
-// The upper halves of a pair: bf16 where the lower ones are zero, else cut off.
-__device__ __forceinline__ uint32_t halves2(f2 v) {
-    float a, b;
-    f2_split(v, a, b);
-    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-}
-__device__ __forceinline__ f2 cut2(f2 v) {
-    float a, b;
-    f2_split(v, a, b);
-    return f2_make(__uint_as_float(__float_as_uint(a) & 0xffff0000u), __uint_as_float(__float_as_uint(b) & 0xffff0000u));
-}
-// w q = hi + mid + lo in bf16 parts for a pair q of bf16: cutting off takes the 24
-// bits apart exactly, 8 at a time, without the conversions (their pipe was 89 % busy
-// with them, and the kernel took NNN times as long).
+// w q = hi + mid + lo in bf16 parts (24 significant bits) for a pair q of bf16
 __device__ __forceinline__ void split3(f2 w, uint32_t q, uint32_t &hi, uint32_t &mid, uint32_t &lo) {
-    f2 v = f2_mul(w, unpack2(q)), t = cut2(v);
-    hi = halves2(t);
-    v = f2_sub(v, t);
-    t = cut2(v);
-    mid = halves2(t);
-    lo = halves2(f2_sub(v, t));
+    f2 v = f2_mul(w, unpack2(q));
+    hi = pack2(v);
+    v = f2_sub(v, unpack2(hi));
+    mid = pack2(v);
+    lo = pack2(f2_sub(v, unpack2(mid)));
 }
 
 __device__ __forceinline__ int ld_acquire(const int *p) {
@@ -428,17 +409,16 @@ struct Finder {
 // call's parameters read inside them, warps waited for instructions half of the
 // time. So what a chunk needs is laid out before the loops (tables, addresses,
 // steps), and the loops are short.
-template <int DX, bool kOwn, int kMode>
-__global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcArgs a,
+template <int DX, bool kOwn, int kMode, bool kF32>
+__global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid_constant__ TcArgs a,
                                                                  const __grid_constant__ TcMaps maps) {
     using M = Smem<DX, kOwn>;
-    using R = Roles<DX>;
     constexpr int NS = M::kStages, KX = DX / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be the same in all lanes)
     const uint32_t sbase = saddr(smem);
-    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * 46);
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + M::oBar + 8 * 48);
     volatile uint32_t *abort_flag = misc + 1;
     Item *items = reinterpret_cast<Item *>(smem + M::oItem);
     float *tabs = reinterpret_cast<float *>(smem + M::oTab);
@@ -449,10 +429,11 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
             int n = 1;
             if (i >= kBarXFree && i < kBarYFree) n = 2;
             else if (i >= kBarYFree && i < kBarZFree) n = kOwn ? 1 : 2;
-            else if (i >= kBarZFree && i < kBarQK) n = kOwn ? R::kV : R::kV + 4;  // the warps of V and E
+            else if (i >= kBarZFree && i < kBarQK) n = 4;  // the warps of E, of V where there is no E
             else if ((i >= kBarP && i < kBarO) || (i >= kBarOFree && i < kBarZs) || i == kBarKVFree || i == kBarS) n = 4;
-            else if ((i >= kBarZs && i < kBarZsFree) || (i >= kBarClear && i < kBarItem)) n = R::kV;
-            else if (i >= kBarItemFree && i < kBarEnd) n = kOwn ? R::kV + 5 : R::kV + 15;  // every role's warps
+            else if ((i >= kBarZs && i < kBarZsFree) || (i >= kBarClear && i < kBarItem)) n = 4;
+            else if (i >= kBarZRead && i < kBarEnd) n = 4;
+            else if (i >= kBarItemFree && i < kBarZRead) n = kOwn ? 9 : 19;  // every role's warps
             bar_init(bars + 8 * i, n);
         }
         misc[1] = 0u;
@@ -741,7 +722,9 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
             each_item([&](const Item &it, const float *tab) {
                 const TcProblem &p = a.p[it.pi];
                 const bool rev = p.rev != 0;
-                const int nc = it.nc, cpart = it.cpart, npart = it.npart, es = p.o_f32 ? 4 : 2;
+                const int nc = it.nc, cpart = it.cpart, npart = it.npart;
+                const bool f32 = kF32 && p.o_f32;
+                const int es = f32 ? 4 : 2;
                 const int bytes = (p.dz - kZ * it.zb < kZ ? p.dz - kZ * it.zb : kZ) * es;  // of a row
                 const int64_t at = (a.seq_start ? 0 : (int64_t)it.seq * p.o_sb) + (int64_t)it.h * p.o_sh + kZ * it.zb +
                                    (int64_t)(it.row0 + t0 + r4) * p.o_sl;
@@ -768,9 +751,10 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
                         for (int i = 0; i < 8; ++i)
                             if (4 * i < nw && off + 16 * q < bytes) *reinterpret_cast<uint4 *>(o + off + i * row4) = v[i];
                     };
-                    if (!wait_all(kBarO + b, cc >> 1)) return false;
+                    // (group V may be behind O_a)
+                    if (!wait_all(kBarO + b, cc >> 1) || !wait_all(kBarZRead + ring.st, ring.use)) return false;
                     tc_after();
-                    if (es == 2) {
+                    if (!f32) {
                         uint32_t r[kZ / 2];
 #pragma unroll
                         for (int i = 0; i < kZ; i += 16) {
@@ -816,7 +800,7 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
         }
     } else if (warp < R::kS0) {
         // ================================= group V =================================
-        constexpr int VT = 32 * R::kV, kItems = kC * 8 / VT / 2;  // 16-byte pieces a thread has in each half
+        constexpr int VT = 128, kItems = kC * 8 / VT / 2;  // 16-byte pieces a thread has in each half
         const int gt = tid - 32 * R::kV0;
         const uint32_t zs = sbase + M::oZs + 16u * gt;
         each_item([&](const Item &it, const float *tab) {
@@ -868,7 +852,7 @@ __global__ void __launch_bounds__(Roles<DX>::kThreads, 1) linattn_tc_kernel(cons
                     __syncwarp();
                     if (lane == 0) {
                         bar_arrive(bar(kBarZs + hf));
-                        if (hf == 1) bar_arrive(bar(kBarZFree + st));
+                        if (hf == 1) bar_arrive(bar((kOwn ? kBarZFree : kBarZRead) + st));
                     }
                 }
             }
@@ -1095,22 +1079,30 @@ Plan plan_of(int64_t batch, int64_t rows, bool packed, int64_t H, int units, int
 // the chains' states.
 size_t flag_bytes(int64_t chains) { return ((size_t)(chains + 1) * sizeof(int) + 255) / 256 * 256; }
 
-template <int DX, bool kOwn, int kMode>
+template <int DX, bool kOwn, int kMode, bool kF32>
 cudaError_t launch_t(const TcArgs &a, const TcMaps &maps, int64_t slots, int num_sms, cudaStream_t stream) {
     static SmemOptIn opt_in;
     constexpr int bytes = Smem<DX, kOwn>::kBytes;
     static_assert(bytes <= 232448, "shared memory of a block");
-    cudaError_t e = opt_in.ensure(reinterpret_cast<const void *>(linattn_tc_kernel<DX, kOwn, kMode>), bytes);
+    cudaError_t e = opt_in.ensure(reinterpret_cast<const void *>(linattn_tc_kernel<DX, kOwn, kMode, kF32>), bytes);
     if (e != cudaSuccess) return e;
     const int64_t items = slots * a.H * a.units;
     if (items > 0x3fffffffLL || a.seg <= 0) return cudaErrorInvalidConfiguration;
-    linattn_tc_kernel<DX, kOwn, kMode><<<(unsigned)std::min<int64_t>(items, num_sms), Roles<DX>::kThreads, bytes, stream>>>(a, maps);
+    linattn_tc_kernel<DX, kOwn, kMode, kF32>
+        <<<(unsigned)std::min<int64_t>(items, num_sms), R::kThreads, bytes, stream>>>(a, maps);
     return cudaGetLastError();
 }
 template <bool kOwn, int kMode>
 cudaError_t launch_dx(int dx, const TcArgs &a, const TcMaps &maps, int64_t slots, int num_sms, cudaStream_t stream) {
-    return dx <= 64 ? launch_t<64, kOwn, kMode>(a, maps, slots, num_sms, stream)
-                    : launch_t<128, kOwn, kMode>(a, maps, slots, num_sms, stream);
+    bool f32 = false;  // (some of the outputs)
+    for (int i = 0; i < a.np; ++i) f32 = f32 || a.p[i].o_f32;
+    if constexpr (!kOwn) {
+        if (f32)
+            return dx <= 64 ? launch_t<64, false, kMode, true>(a, maps, slots, num_sms, stream)
+                            : launch_t<128, false, kMode, true>(a, maps, slots, num_sms, stream);
+    }
+    return dx <= 64 ? launch_t<64, kOwn, kMode, false>(a, maps, slots, num_sms, stream)
+                    : launch_t<128, kOwn, kMode, false>(a, maps, slots, num_sms, stream);
 }
 
 }  // namespace

@@ -274,6 +274,23 @@ def test_same_bits_again_and_in_a_graph():
     assert all(torch.equal(a, b) for a, b in zip(first, held))
 
 
+@pytest.mark.parametrize("b,L,H,G,dk,dv", [(8, 700, 24, 24, 64, 64), (3, 1100, 20, 10, 128, 128), (1, 4000, 3, 3, 64, 128)])
+def test_same_bits_over_many_runs(b, L, H, G, dk, dv):
+    """Items that change hands between CTAs, roles that run ahead of one another: never another bit."""
+    gen = torch.Generator(device=DEV).manual_seed(b * L)
+    r = lambda n, d: torch.randn(b, L, n, d, device=DEV, generator=gen).to(BF)  # noqa: E731
+    q, k, v, do = r(H, dk), r(G, dk), r(G, dv), r(H, dv)
+    g = -torch.rand(H, device=DEV, generator=gen) * 0.05
+
+    def step():
+        o, fin = mb.linattn_fwd(q, k, v, g)
+        gr = mb.linattn_bwd(q, k, v, g, do)
+        return [o, fin, gr["dq"], gr["dk"], gr["dv"], gr["dinitial_state"]]
+    first = step()
+    for _ in range(15):
+        assert all(torch.equal(a, c) for a, c in zip(first, step()))
+
+
 # ------------------------------------------------------------- single tokens ----
 
 @pytest.mark.parametrize("dtype", [BF, F32])
