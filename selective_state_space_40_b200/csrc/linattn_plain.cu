@@ -146,59 +146,75 @@ __global__ void __launch_bounds__(256) linattn_reduce_kernel(const LaReduceArgs 
 // ------------------------------------------------------------ one token ----
 
 constexpr int kUThr = 256;
+constexpr int kURows = 8;   // rows of the state that a thread has on their way
+constexpr int kUDk = 256;   // rows whose k and q wait in shared memory at a time
 
 // S = lam S + k v^T and o = a q S for one (row, head): the state is read and
 // written once, which bounds it (HBM). A thread owns VEC neighbouring columns
-// and every rp-th row; its first kURows loads are in flight together; the
-// column sums of q S meet in shared memory.
-constexpr int kURows = 8;
+// and every rp-th row; its state is on its way before anything else is read,
+// k and q go through shared memory, and the column sums of q S meet there.
+// Back-to-back steps overlap through programmatic dependent launch.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kUThr) linattn_update_kernel(const LaUpdateArgs a, int cg) {
+    // the next grid may be scheduled; what the previous one wrote is waited for before any read
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t b = blockIdx.x / a.H, h = blockIdx.x % a.H, g = h / (a.H / a.kv);
     const int col = threadIdx.x % cg, r0 = threadIdx.x / cg, rp = kUThr / cg;
     const int e0 = col * VEC;
-    __shared__ float red[kUThr * VEC];
+    __shared__ __align__(16) float red[kUThr * VEC], ks[kUDk], qs[kUDk];
     const T *q = static_cast<const T *>(a.q) + b * a.q_sb + h * a.q_sh;
     const T *k = static_cast<const T *>(a.k) + b * a.k_sb + g * a.k_sh;
     const T *v = static_cast<const T *>(a.v) + b * a.v_sb + g * a.v_sh;
     float *st = a.state + b * a.st_sb + h * a.st_sh + e0;
     const bool live = e0 < a.dv;
-    const Decay lam = decay_of(__ldg(a.log_decay + h));
-    float acc[VEC], vv[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-        acc[j] = 0.0f;
-        vv[j] = live ? Elem<T>::load(v + e0 + j) : 0.0f;
-    }
-    for (int i0 = r0; live && i0 < a.dk; i0 += rp * kURows) {
-        float s[kURows][VEC], kk[kURows], qq[kURows];
+    float s[kURows][VEC], acc[VEC], vv[VEC];
+    auto fetch = [&](int i0, int end) {
 #pragma unroll
         for (int u = 0; u < kURows; ++u) {
             const int i = i0 + u * rp;
-            if (i < a.dk) {
+            if (live && i < end) {
                 if constexpr (VEC == 4) {
                     const float4 t = *reinterpret_cast<const float4 *>(st + (int64_t)i * a.dv);
                     s[u][0] = t.x; s[u][1] = t.y; s[u][2] = t.z; s[u][3] = t.w;
                 } else {
                     s[u][0] = st[(int64_t)i * a.dv];
                 }
-                kk[u] = Elem<T>::load(k + i);
-                qq[u] = Elem<T>::load(q + i);
             }
         }
+    };
+    fetch(r0, a.dk < kUDk ? a.dk : kUDk);
+    const Decay lam = decay_of(__ldg(a.log_decay + h));
 #pragma unroll
-        for (int u = 0; u < kURows; ++u) {
-            const int i = i0 + u * rp;
-            if (i < a.dk) {
+    for (int j = 0; j < VEC; ++j) {
+        acc[j] = 0.0f;
+        vv[j] = live ? Elem<T>::load(v + e0 + j) : 0.0f;
+    }
+    for (int d0 = 0; d0 < a.dk; d0 += kUDk) {
+        if (d0) __syncthreads();
+        if (d0 + (int)threadIdx.x < a.dk) {
+            ks[threadIdx.x] = Elem<T>::load(k + d0 + threadIdx.x);
+            qs[threadIdx.x] = Elem<T>::load(q + d0 + threadIdx.x);
+        }
+        __syncthreads();
+        const int end = a.dk < d0 + kUDk ? a.dk : d0 + kUDk;
+        for (int i0 = d0 + r0; i0 < end; i0 += rp * kURows) {  // (rp divides kUDk)
+            if (i0 != r0) fetch(i0, end);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    s[u][j] = decayed(s[u][j], lam, kk[u] * vv[j]);
-                    acc[j] = fmaf(qq[u], s[u][j], acc[j]);
+            for (int u = 0; u < kURows; ++u) {
+                const int i = i0 + u * rp;
+                if (live && i < end) {
+                    const float kk = ks[i - d0], qq = qs[i - d0];
+#pragma unroll
+                    for (int j = 0; j < VEC; ++j) {
+                        s[u][j] = decayed(s[u][j], lam, kk * vv[j]);
+                        acc[j] = fmaf(qq, s[u][j], acc[j]);
+                    }
+                    if constexpr (VEC == 4)
+                        *reinterpret_cast<float4 *>(st + (int64_t)i * a.dv) = make_float4(s[u][0], s[u][1], s[u][2], s[u][3]);
+                    else
+                        st[(int64_t)i * a.dv] = s[u][0];
                 }
-                if constexpr (VEC == 4)
-                    *reinterpret_cast<float4 *>(st + (int64_t)i * a.dv) = make_float4(s[u][0], s[u][1], s[u][2], s[u][3]);
-                else
-                    st[(int64_t)i * a.dv] = s[u][0];
             }
         }
     }
@@ -206,9 +222,9 @@ __global__ void __launch_bounds__(kUThr) linattn_update_kernel(const LaUpdateArg
     for (int j = 0; j < VEC; ++j) red[r0 * cg * VEC + e0 + j] = acc[j];
     __syncthreads();
     for (int e = threadIdx.x; e < a.dv; e += kUThr) {
-        float s = 0.0f;
-        for (int r = 0; r < rp; ++r) s += red[r * cg * VEC + e];
-        Elem<T>::store(static_cast<T *>(a.o) + b * a.o_sb + h * a.o_sh + e, a.scale * s);
+        float t = 0.0f;
+        for (int r = 0; r < rp; ++r) t += red[r * cg * VEC + e];
+        Elem<T>::store(static_cast<T *>(a.o) + b * a.o_sb + h * a.o_sh + e, a.scale * t);
     }
 }
 
@@ -222,9 +238,17 @@ cudaError_t launch_update_t(const LaUpdateArgs &a, cudaStream_t stream) {
     int cg = 1;
     while (cg < cols) cg *= 2;
     if (cg > kUThr) return cudaErrorInvalidConfiguration;
-    if (vec) linattn_update_kernel<T, 4><<<(unsigned)blocks, kUThr, 0, stream>>>(a, cg);
-    else linattn_update_kernel<T, 1><<<(unsigned)blocks, kUThr, 0, stream>>>(a, cg);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kUThr);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return vec ? cudaLaunchKernelEx(&cfg, linattn_update_kernel<T, 4>, a, cg)
+               : cudaLaunchKernelEx(&cfg, linattn_update_kernel<T, 1>, a, cg);
 }
 
 }  // namespace

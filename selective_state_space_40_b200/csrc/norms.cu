@@ -30,29 +30,63 @@ namespace ms {
 namespace {
 
 constexpr int kMaxThr = 512;  // threads of a block, at most
+// Registers of a thread: with 96, blocks of 320 threads (5120 bf16 columns) run two to an
+// SM and have 60 KB of rows on their way; the wider rows' threads hold more of them.
+template <int NV>
+constexpr int kRegs = NV <= 1 ? 64 : NV <= 2 ? 96 : 128;
 
+// VEC neighbouring elements as they lie in memory: a row waits in this form.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        v[0] = Elem<T>::load(p);
-    } else if constexpr (sizeof(T) == 2) {
-        static_assert(VEC % 8 == 0, "");
+struct Raw {
+    uint4 v[VEC * sizeof(T) / 16];
+    __device__ __forceinline__ void load(const T *p, bool on) {
 #pragma unroll
-        for (int q = 0; q < VEC / 8; ++q) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p) + q);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int q = 0; q < (int)(VEC * sizeof(T) / 16); ++q)
+            v[q] = on ? __ldg(reinterpret_cast<const uint4 *>(p) + q) : make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void load_shared(uint32_t at, bool on) {
+#pragma unroll
+        for (int q = 0; q < (int)(VEC * sizeof(T) / 16); ++q) {
+            v[q] = make_uint4(0, 0, 0, 0);
+            if (on)
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v[q].x), "=r"(v[q].y), "=r"(v[q].z), "=r"(v[q].w)
+                             : "r"(at + 16u * q)
+                             : "memory");
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[VEC]) const {
+#pragma unroll
+        for (int q = 0; q < (int)(VEC * sizeof(T) / 16); ++q) {
+            const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[8 * q + 2 * i] = bf16_lo(u[i]);
-                v[8 * q + 2 * i + 1] = bf16_hi(u[i]);
+                if constexpr (sizeof(T) == 2) {
+                    f[8 * q + 2 * i] = bf16_lo(u[i]);
+                    f[8 * q + 2 * i + 1] = bf16_hi(u[i]);
+                } else {
+                    f[4 * q + i] = __uint_as_float(u[i]);
+                }
             }
         }
-    } else {
+    }
+};
+template <typename T>
+struct Raw<T, 1> {
+    float v;
+    __device__ __forceinline__ void load(const T *p, bool on) { v = on ? Elem<T>::load(p) : 0.0f; }
+    __device__ __forceinline__ void load_shared(uint32_t, bool) {}  // (rings carry whole vectors)
+    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = v; }
+};
+// fp32 weights of VEC columns, 1 where there are none
+template <int VEC>
+__device__ __forceinline__ void weights(const float *w, bool on, float (&f)[VEC]) {
 #pragma unroll
-        for (int q = 0; q < VEC / 4; ++q) {
-            const float4 w = __ldg(reinterpret_cast<const float4 *>(p) + q);
-            v[4 * q] = w.x; v[4 * q + 1] = w.y; v[4 * q + 2] = w.z; v[4 * q + 3] = w.w;
-        }
+    for (int i = 0; i < VEC; ++i) f[i] = 1.0f;
+    if (w && on) {
+        Raw<float, VEC> r;
+        r.load(w, true);
+        r.get(f);
     }
 }
 template <typename T, int VEC>
@@ -77,6 +111,67 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
     }
 }
 
+// Rows on their way through shared memory: NA arrays' rows a stage, brought by bulk
+// copies, so that several rows of a block are in flight without holding registers
+// (the gated backward of 5120 bf16 columns: NNN us, NNN with one row in registers).
+// For blocks of one group; row k of a block is in stage k % stages, phase k / stages.
+template <int NA>
+struct Ring {
+    uint32_t data, bars, stage_bytes;
+    uint32_t bytes[NA];  // of each array's row (0: not there)
+    int stages;
+    __device__ __forceinline__ uint32_t bar(int st) const { return bars + 8u * (uint32_t)st; }
+    // by every thread, with a barrier behind it
+    __device__ __forceinline__ void init(unsigned char *smem, int n) {
+        stages = n;
+        bars = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+        data = bars + 128u;
+        stage_bytes = 0;
+#pragma unroll
+        for (int i = 0; i < NA; ++i) stage_bytes += bytes[i];
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < n; ++i)
+                asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar(i)) : "memory");
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ void issue(int st, const void *const (&src)[NA]) const {
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar(st)), "r"(stage_bytes) : "memory");
+        uint32_t at = data + (uint32_t)st * stage_bytes;
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            if (bytes[i])
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(at),
+                             "l"(src[i]), "r"(bytes[i]), "r"(bar(st))
+                             : "memory");
+            at += bytes[i];
+        }
+    }
+    // bounded: on a timeout MS_ERR_TIMEOUT is recorded and the row is not valid
+    __device__ __forceinline__ void wait(int st, uint32_t phase, int *status) const {
+        for (uint32_t i = 0; i < (1u << 20); ++i) {
+            uint32_t done;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(bar(st)), "r"(phase & 1u)
+                : "memory");
+            if (done) return;
+        }
+        if (status) atomicOr(status, MS_ERR_TIMEOUT);
+    }
+    // shared address of array i's row in a stage
+    __device__ __forceinline__ uint32_t row(int st, int i) const {
+        uint32_t at = data + (uint32_t)st * stage_bytes;
+#pragma unroll
+        for (int k = 0; k < NA; ++k)
+            if (k < i) at += bytes[k];
+        return at;
+    }
+};
+
 // How a launch lays threads over rows and columns.
 struct NormPlan {
     int tpr;      // threads per group: a power of two up to 32, or a multiple of 32
@@ -85,27 +180,30 @@ struct NormPlan {
     int gblocks;  // column blocks
     int rblocks;  // row blocks
     int W;        // columns per group
+    int stages;   // rows of a block's ring (0: rows go straight to registers)
 };
 
 // Sums of NS values over the tpr threads of a group, the same in every thread.
+// `sm` holds two rows' sums of the warps, used in turn: one barrier a row.
+constexpr int kMaxWarps = kMaxThr / 32;
 template <int NS>
-__device__ __forceinline__ void group_sum(float (&s)[NS], int tpr, float *sm) {
+__device__ __forceinline__ void group_sum(float (&s)[NS], int tpr, float (*sm)[2 * kMaxWarps], int &turn) {
     const int width = tpr < 32 ? tpr : 32;
     for (int off = width >> 1; off > 0; off >>= 1)
 #pragma unroll
         for (int i = 0; i < NS; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
     if (tpr > 32) {
-        const int warp = threadIdx.x >> 5, wpg = tpr >> 5, w0 = warp / wpg * wpg;
-        __syncthreads();  // the last row's sums have been read
+        const int warp = threadIdx.x >> 5, warps = tpr >> 5;  // (one group a block)
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
-            for (int i = 0; i < NS; ++i) sm[NS * warp + i] = s[i];
+            for (int i = 0; i < NS; ++i) sm[turn][NS * warp + i] = s[i];
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NS; ++i) s[i] = 0.0f;
-        for (int w = w0; w < w0 + wpg; ++w)
+        for (int w = 0; w < warps; ++w)
 #pragma unroll
-            for (int i = 0; i < NS; ++i) s[i] += sm[NS * w + i];
+            for (int i = 0; i < NS; ++i) s[i] += sm[turn][NS * w + i];
+        turn ^= 1;
     }
 }
 
@@ -129,248 +227,428 @@ __device__ __forceinline__ Place place_of(const NormPlan &pl, int64_t groups) {
     return p;
 }
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kMaxThr) gated_norm_fwd_kernel(const GatedNormArgs a, const NormPlan pl) {
-    __shared__ float sm[32];
+// How the gate takes part: not at all, behind the norm, or in front of it.
+enum { kNoGate = 0, kGateBehind = 1, kGateFirst = 2 };
+__device__ __forceinline__ float sigmoid_f(float z) { return rcp_mufu(1.0f + exp2_mufu(-z * kLog2e)); }
+
+// The rows of a block are read one ahead of the row in work where the registers
+// allow it: a row's sums wait for all of its columns.
+template <int VEC, int NV, bool RING>
+constexpr bool kAhead = !RING && VEC *NV <= 16;
+
+template <typename T, int VEC, int NV, bool RING, int GATE>
+__global__ void __maxnreg__(kRegs<NV>) gated_norm_fwd_kernel(const GatedNormArgs a, const NormPlan pl) {
+    __shared__ float sm[2][2 * kMaxWarps];
+    int turn = 0;
     const Place p = place_of<VEC>(pl, a.groups);
     const float invW = 1.0f / (float)pl.W;
-    const int64_t col = p.g * pl.W;
+    const int64_t col = p.g * pl.W + p.c0, dr = (int64_t)gridDim.x * pl.ty;
+    const int dc = pl.tpr * VEC;
+    bool in[NV];
     float w[NV][VEC];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-            w[j][i] = (a.w && p.live && c < pl.W) ? __ldg(a.w + col + c + i) : 1.0f;
-        }
-    for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += (int64_t)gridDim.x * pl.ty) {
-        const int64_t r = r0 + p.ty;
-        const bool on = p.live && r < a.rows;
-        float x[NV][VEC], gt[NV][VEC], s[1] = {0.0f};
+    for (int j = 0; j < NV; ++j) {
+        in[j] = p.live && p.c0 + j * dc < pl.W;
+        weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], w[j]);
+    }
+    Raw<T, VEC> rx[NV], rz[NV], nx[NV], nz[NV];
+    const T *x = static_cast<const T *>(a.x) + col, *z = static_cast<const T *>(a.z) + col;
+    auto fetch = [&](int64_t r, Raw<T, VEC> (&fx)[NV], Raw<T, VEC> (&fz)[NV]) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = p.c0 + j * pl.tpr * VEC;
+            const bool on = in[j] && r < a.rows;
+            fx[j].load(x + r * a.x_sr + j * dc, on);
+            if constexpr (GATE != kNoGate) fz[j].load(z + r * a.z_sr + j * dc, on);
+        }
+    };
+    extern __shared__ __align__(128) unsigned char ring_smem[];
+    Ring<2> ring;
+    int st = 0;  // the row's stage, and its phase
+    uint32_t phase = 0;
+    auto refill = [&](int stage, int64_t row) {
+        const void *const src[2] = {static_cast<const T *>(a.x) + row * a.x_sr + p.g * pl.W, static_cast<const T *>(a.z) + row * a.z_sr + p.g * pl.W};
+        ring.issue(stage, src);
+    };
+    if constexpr (RING) {
+        ring.bytes[0] = pl.W * (uint32_t)sizeof(T);
+        ring.bytes[1] = GATE != kNoGate ? ring.bytes[0] : 0u;
+        ring.init(ring_smem, pl.stages);
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int i = 0; i < pl.stages; ++i)
+                if (blockIdx.x + i * dr < a.rows) refill(i, blockIdx.x + i * dr);
+    }
+    int64_t r = (int64_t)blockIdx.x * pl.ty + p.ty;
+    if (kAhead<VEC, NV, RING>) fetch(r, rx, rz);
+    for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += dr, r += dr) {
+        if (kAhead<VEC, NV, RING>) fetch(r + dr, nx, nz);
+        else if constexpr (!RING) fetch(r, rx, rz);
+        if constexpr (RING) {
+            ring.wait(st, phase, a.status);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) x[j][i] = 0.0f, gt[j][i] = 1.0f;
-            if (on && c < pl.W) {
-                load_vec<T, VEC>(static_cast<const T *>(a.x) + r * a.x_sr + col + c, x[j]);
-                if (a.z) {
-                    load_vec<T, VEC>(static_cast<const T *>(a.z) + r * a.z_sr + col + c, gt[j]);
+            for (int j = 0; j < NV; ++j) {
+                rx[j].load_shared(ring.row(st, 0) + (p.c0 + j * dc) * (uint32_t)sizeof(T), in[j]);
+                if constexpr (GATE != kNoGate) rz[j].load_shared(ring.row(st, 1) + (p.c0 + j * dc) * (uint32_t)sizeof(T), in[j]);
+            }
+        }
+        float v[NV][VEC], s[1] = {0.0f};
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        gt[j][i] = silu_f(gt[j][i]);
-                        if (a.gate_first) x[j][i] *= gt[j][i];
+        for (int j = 0; j < NV; ++j) {
+            rx[j].get(v[j]);
+            if constexpr (GATE == kGateFirst) {
+                float g[VEC];
+                rz[j].get(g);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[j][i] *= silu_f(g[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) s[0] = fmaf(v[j][i], v[j][i], s[0]);
+        }
+        group_sum<1>(s, pl.tpr, sm, turn);
+        if constexpr (RING) {
+            // every thread has read the row: its place is the next one's
+            if (threadIdx.x == 0 && r + pl.stages * dr < a.rows) refill(st, r + pl.stages * dr);
+            if (++st == pl.stages) st = 0, ++phase;
+        }
+        const float inv = rsqrtf(fmaf(s[0], invW, a.eps));
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[j][i] *= inv * w[j][i];
+            if constexpr (GATE == kGateBehind) {
+                float g[VEC];
+                rz[j].get(g);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) v[j][i] *= silu_f(g[i]);
+            }
+            if (in[j] && r < a.rows) store_vec<T, VEC>(static_cast<T *>(a.y) + r * a.y_sr + col + j * dc, v[j]);
+            if (kAhead<VEC, NV, RING>) rx[j] = nx[j], rz[j] = nz[j];
+        }
+    }
+}
+
+template <typename T, int VEC, int NV, bool RING, int GATE>
+__global__ void __maxnreg__(kRegs<NV>) gated_norm_bwd_kernel(const GatedNormArgs a, const NormPlan pl) {
+    __shared__ float sm[2][2 * kMaxWarps];
+    int turn = 0;
+    const Place p = place_of<VEC>(pl, a.groups);
+    const float invW = 1.0f / (float)pl.W;
+    const int64_t col = p.g * pl.W + p.c0, dr = (int64_t)gridDim.x * pl.ty;
+    const int dc = pl.tpr * VEC;
+    bool in[NV];
+    float dw[NV][VEC];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        in[j] = p.live && p.c0 + j * dc < pl.W;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dw[j][i] = 0.0f;
+    }
+    Raw<T, VEC> rx[NV], rz[NV], ry[NV];
+    const T *x = static_cast<const T *>(a.x) + col, *z = static_cast<const T *>(a.z) + col;
+    const T *dy = static_cast<const T *>(a.dy) + col;
+    const float *wt = a.w ? a.w + col : nullptr;  // read again for every row (it stays in L1)
+    extern __shared__ __align__(128) unsigned char ring_smem[];
+    Ring<3> ring;
+    int st = 0;  // the row's stage, and its phase
+    uint32_t phase = 0;
+    auto refill = [&](int stage, int64_t row) {
+        const void *const src[3] = {static_cast<const T *>(a.x) + row * a.x_sr + p.g * pl.W, static_cast<const T *>(a.dy) + row * a.y_sr + p.g * pl.W,
+                                     static_cast<const T *>(a.z) + row * a.z_sr + p.g * pl.W};
+        ring.issue(stage, src);
+    };
+    if constexpr (RING) {
+        ring.bytes[0] = ring.bytes[1] = pl.W * (uint32_t)sizeof(T);
+        ring.bytes[2] = GATE != kNoGate ? ring.bytes[0] : 0u;
+        ring.init(ring_smem, pl.stages);
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int i = 0; i < pl.stages; ++i)
+                if (blockIdx.x + i * dr < a.rows) refill(i, blockIdx.x + i * dr);
+    }
+    int64_t r = (int64_t)blockIdx.x * pl.ty + p.ty;
+    for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += dr, r += dr) {
+        float s[2] = {0.0f, 0.0f};
+        if constexpr (RING) ring.wait(st, phase, a.status);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const bool on = in[j] && r < a.rows;
+            if constexpr (RING) {
+                const uint32_t at = (p.c0 + j * dc) * (uint32_t)sizeof(T);
+                rx[j].load_shared(ring.row(st, 0) + at, on);
+                ry[j].load_shared(ring.row(st, 1) + at, on);
+                if constexpr (GATE != kNoGate) rz[j].load_shared(ring.row(st, 2) + at, on);
+                continue;
+            }
+            rx[j].load(x + r * a.x_sr + j * dc, on);
+            ry[j].load(dy + r * a.y_sr + j * dc, on);
+            if constexpr (GATE != kNoGate) rz[j].load(z + r * a.z_sr + j * dc, on);
+        }
+        // u: the normed value; gr: the gradient of n(u) w; sig: silu(z) = z sig, of which both
+        // passes need, kept between them (the formulas' instructions, not HBM, bound this kernel)
+        float sig[NV][GATE != kNoGate ? VEC : 1];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float u[VEC], gr[VEC], z_[VEC], w[VEC];
+            rx[j].get(u);
+            ry[j].get(gr);
+            weights<VEC>(wt ? wt + j * dc : nullptr, in[j], w);
+            if constexpr (GATE != kNoGate) {
+                rz[j].get(z_);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    sig[j][i] = sigmoid_f(z_[i]);
+                    if constexpr (GATE == kGateFirst) u[i] *= z_[i] * sig[j][i];
+                    else gr[i] *= z_[i] * sig[j][i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                s[0] = fmaf(u[i], u[i], s[0]);
+                s[1] = fmaf(gr[i] * w[i], u[i], s[1]);
+            }
+        }
+        group_sum<2>(s, pl.tpr, sm, turn);
+        if constexpr (RING) {
+            // every thread has read the row: its place is the next one's
+            if (threadIdx.x == 0 && r + pl.stages * dr < a.rows) refill(st, r + pl.stages * dr);
+            if (++st == pl.stages) st = 0, ++phase;
+        }
+        const float inv = rsqrtf(fmaf(s[0], invW, a.eps));
+        const float k = inv * inv * s[1] * invW;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float u[VEC], gr[VEC], z_[VEC], w[VEC], dz[VEC];
+            rx[j].get(u);
+            ry[j].get(gr);
+            weights<VEC>(wt ? wt + j * dc : nullptr, in[j], w);
+            if constexpr (GATE != kNoGate) rz[j].get(z_);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                if constexpr (GATE == kNoGate) {
+                    dw[j][i] = fmaf(gr[i], u[i] * inv, dw[j][i]);
+                    u[i] = inv * fmaf(-k, u[i], gr[i] * w[i]);
+                } else {
+                    // silu' = sig (1 + z (1 - sig)) = sig + silu (1 - sig)
+                    const float sg = sig[j][i], gate = z_[i] * sg, slope = fmaf(gate, 1.0f - sg, sg);
+                    if constexpr (GATE == kGateFirst) {
+                        const float n = u[i] * gate, du = inv * fmaf(-k, n, gr[i] * w[i]);
+                        dw[j][i] = fmaf(gr[i], n * inv, dw[j][i]);
+                        dz[i] = du * u[i] * slope;
+                        u[i] = du * gate;
+                    } else {
+                        const float hat = u[i] * inv, gi = gr[i] * gate;
+                        dw[j][i] = fmaf(gi, hat, dw[j][i]);
+                        dz[i] = gr[i] * hat * w[i] * slope;
+                        u[i] = inv * fmaf(-k, u[i], gi * w[i]);
                     }
                 }
             }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) s[0] = fmaf(x[j][i], x[j][i], s[0]);
-        }
-        group_sum<1>(s, pl.tpr, sm);
-        const float inv = rsqrtf(fmaf(s[0], invW, a.eps));
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-            if (on && c < pl.W) {
-                float y[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) y[i] = x[j][i] * inv * w[j][i] * (a.gate_first ? 1.0f : gt[j][i]);
-                store_vec<T, VEC>(static_cast<T *>(a.y) + r * a.y_sr + col + c, y);
+            if (in[j] && r < a.rows) {
+                store_vec<T, VEC>(static_cast<T *>(a.dx) + r * a.width + col + j * dc, u);
+                if constexpr (GATE != kNoGate) store_vec<T, VEC>(static_cast<T *>(a.dz) + r * a.width + col + j * dc, dz);
             }
         }
     }
-}
-
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kMaxThr) gated_norm_bwd_kernel(const GatedNormArgs a, const NormPlan pl) {
-    __shared__ float sm[64];
-    const Place p = place_of<VEC>(pl, a.groups);
-    const float invW = 1.0f / (float)pl.W;
-    const int64_t col = p.g * pl.W;
-    float w[NV][VEC], dw[NV][VEC];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-            w[j][i] = (a.w && p.live && c < pl.W) ? __ldg(a.w + col + c + i) : 1.0f;
-            dw[j][i] = 0.0f;
-        }
-    for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += (int64_t)gridDim.x * pl.ty) {
-        const int64_t r = r0 + p.ty;
-        const bool on = p.live && r < a.rows;
-        float x[NV][VEC], z[NV][VEC], dy[NV][VEC], s[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) x[j][i] = z[j][i] = dy[j][i] = 0.0f;
-            if (on && c < pl.W) {
-                load_vec<T, VEC>(static_cast<const T *>(a.x) + r * a.x_sr + col + c, x[j]);
-                load_vec<T, VEC>(static_cast<const T *>(a.dy) + r * a.y_sr + col + c, dy[j]);
-                if (a.z) load_vec<T, VEC>(static_cast<const T *>(a.z) + r * a.z_sr + col + c, z[j]);
-            }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                // u: the normed value; gr: the gradient of n(u) w
-                const float gate = a.z ? silu_f(z[j][i]) : 1.0f;
-                const float u = a.gate_first ? x[j][i] * gate : x[j][i];
-                const float gr = a.gate_first ? dy[j][i] : dy[j][i] * gate;
-                s[0] = fmaf(u, u, s[0]);
-                s[1] = fmaf(gr * w[j][i], u, s[1]);
-            }
-        }
-        group_sum<2>(s, pl.tpr, sm);
-        const float inv = rsqrtf(fmaf(s[0], invW, a.eps));
-        const float k = inv * inv * s[1] * invW;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-            if (on && c < pl.W) {
-                float dx[VEC], dz[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    // silu = z sig, silu' = sig (1 + z (1 - sig))
-                    const float sig = a.z ? rcp_mufu(1.0f + exp2_mufu(-z[j][i] * kLog2e)) : 1.0f;
-                    const float gate = a.z ? z[j][i] * sig : 1.0f;
-                    const float slope = sig * fmaf(z[j][i], 1.0f - sig, 1.0f);
-                    const float u = a.gate_first ? x[j][i] * gate : x[j][i];
-                    const float gr = a.gate_first ? dy[j][i] : dy[j][i] * gate;
-                    const float du = inv * fmaf(-k, u, gr * w[j][i]);
-                    const float hat = u * inv;
-                    dw[j][i] = fmaf(gr, hat, dw[j][i]);
-                    dx[i] = a.gate_first ? du * gate : du;
-                    dz[i] = (a.gate_first ? du * x[j][i] : dy[j][i] * hat * w[j][i]) * slope;
-                }
-                store_vec<T, VEC>(static_cast<T *>(a.dx) + r * a.width + col + c, dx);
-                if (a.z) store_vec<T, VEC>(static_cast<T *>(a.dz) + r * a.width + col + c, dz);
-            }
-        }
-    }
-    if (a.dw && p.live) {
+    if (a.dw) {
         float *part = a.part + ((int64_t)blockIdx.x * pl.ty + p.ty) * a.width + col;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-            if (c < pl.W) store_vec<float, VEC>(part + c, dw[j]);
-        }
+        for (int j = 0; j < NV; ++j)
+            if (in[j]) store_vec<float, VEC>(part + j * dc, dw[j]);
     }
 }
 
-template <typename T, typename R, int VEC, int NV>
-__global__ void __launch_bounds__(kMaxThr) residual_norm_fwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
-    __shared__ float sm[32];
+template <typename T, typename R, int VEC, int NV, bool RING>
+__global__ void __maxnreg__(kRegs<NV>) residual_norm_fwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
+    __shared__ float sm[2][2 * kMaxWarps];
+    int turn = 0;
     const Place p = place_of<VEC>(pl, 1);
     const float invW = 1.0f / (float)pl.W;
-    for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += (int64_t)gridDim.x * pl.ty) {
-        const int64_t r = r0 + p.ty;
-        const bool on = r < a.rows;
+    const int64_t col = p.c0, dr = (int64_t)gridDim.x * pl.ty;
+    const int dc = pl.tpr * VEC;
+    bool in[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) in[j] = p.c0 + j * dc < pl.W;
+    Raw<T, VEC> rx[NV], nx[NV];
+    Raw<R, VEC> rr[NV], nr[NV];
+    auto fetch = [&](int64_t r, Raw<T, VEC> (&fx)[NV], Raw<R, VEC> (&fr)[NV]) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const bool on = in[j] && r < a.rows;
+            fx[j].load(static_cast<const T *>(a.x) + r * a.x_sr + col + j * dc, on);
+            fr[j].load(static_cast<const R *>(a.res) + r * a.res_sr + col + j * dc, on && a.res);
+        }
+    };
+    extern __shared__ __align__(128) unsigned char ring_smem[];
+    Ring<2> ring;
+    int st = 0;  // the row's stage, and its phase
+    uint32_t phase = 0;
+    auto refill = [&](int stage, int64_t row) {
+        const void *const src[2] = {static_cast<const T *>(a.x) + row * a.x_sr, static_cast<const R *>(a.res) + row * a.res_sr};
+        ring.issue(stage, src);
+    };
+    if constexpr (RING) {
+        ring.bytes[0] = pl.W * (uint32_t)sizeof(T);
+        ring.bytes[1] = a.res ? pl.W * (uint32_t)sizeof(R) : 0u;
+        ring.init(ring_smem, pl.stages);
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int i = 0; i < pl.stages; ++i)
+                if (blockIdx.x + i * dr < a.rows) refill(i, blockIdx.x + i * dr);
+    }
+    int64_t r = (int64_t)blockIdx.x * pl.ty + p.ty;
+    if (kAhead<VEC, NV, RING>) fetch(r, rx, rr);
+    for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += dr, r += dr) {
+        if (kAhead<VEC, NV, RING>) fetch(r + dr, nx, nr);
+        else if constexpr (!RING) fetch(r, rx, rr);
+        if constexpr (RING) {
+            ring.wait(st, phase, a.status);
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                rx[j].load_shared(ring.row(st, 0) + (p.c0 + j * dc) * (uint32_t)sizeof(T), in[j]);
+                rr[j].load_shared(ring.row(st, 1) + (p.c0 + j * dc) * (uint32_t)sizeof(R), in[j] && a.res);
+            }
+        }
         float h[NV][VEC], s[1] = {0.0f};
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-            float x[VEC];
+            float x[VEC], c[VEC];
+            rx[j].get(x);
+            rr[j].get(h[j]);
+            weights<VEC>(a.cs ? a.cs + col + j * dc : nullptr, in[j], c);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) h[j][i] = x[i] = 0.0f;
-            if (on && c < pl.W) {
-                load_vec<T, VEC>(static_cast<const T *>(a.x) + r * a.x_sr + c, x);
-                if (a.res) load_vec<R, VEC>(static_cast<const R *>(a.res) + r * a.res_sr + c, h[j]);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    h[j][i] = fmaf(a.cs ? a.scale * __ldg(a.cs + c + i) : a.scale, x[i], h[j][i]);
-                if (a.res_out) store_vec<R, VEC>(static_cast<R *>(a.res_out) + r * a.ro_sr + c, h[j]);
+            for (int i = 0; i < VEC; ++i) {
+                h[j][i] = fmaf(a.scale * c[i], x[i], h[j][i]);
+                s[0] = fmaf(h[j][i], h[j][i], s[0]);
             }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) s[0] = fmaf(h[j][i], h[j][i], s[0]);
+            if (in[j] && r < a.rows && a.res_out)
+                store_vec<R, VEC>(static_cast<R *>(a.res_out) + r * a.ro_sr + col + j * dc, h[j]);
         }
-        group_sum<1>(s, pl.tpr, sm);
+        group_sum<1>(s, pl.tpr, sm, turn);
+        if constexpr (RING) {
+            // every thread has read the row: its place is the next one's
+            if (threadIdx.x == 0 && r + pl.stages * dr < a.rows) refill(st, r + pl.stages * dr);
+            if (++st == pl.stages) st = 0, ++phase;
+        }
         const float inv = rsqrtf(fmaf(s[0], invW, a.eps));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-            if (on && c < pl.W) {
-                float y[VEC];
+            float w[VEC];
+            weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], w);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) y[i] = h[j][i] * inv * (a.w ? __ldg(a.w + c + i) : 1.0f);
-                store_vec<T, VEC>(static_cast<T *>(a.y) + r * a.y_sr + c, y);
-            }
+            for (int i = 0; i < VEC; ++i) h[j][i] *= inv * w[i];
+            if (in[j] && r < a.rows) store_vec<T, VEC>(static_cast<T *>(a.y) + r * a.y_sr + col + j * dc, h[j]);
+            if (kAhead<VEC, NV, RING>) rx[j] = nx[j], rr[j] = nr[j];
         }
     }
 }
 
-template <typename T, typename R, int VEC, int NV>
-__global__ void __launch_bounds__(kMaxThr) residual_norm_bwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
-    __shared__ float sm[64];
+template <typename T, typename R, int VEC, int NV, bool RING>
+__global__ void __maxnreg__(kRegs<NV>) residual_norm_bwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
+    __shared__ float sm[2][2 * kMaxWarps];
+    int turn = 0;
     const Place p = place_of<VEC>(pl, 1);
     const float invW = 1.0f / (float)pl.W;
-    float w[NV][VEC], dw[NV][VEC], dc[NV][VEC];
+    const int64_t col = p.c0, dr = (int64_t)gridDim.x * pl.ty;
+    const int dc = pl.tpr * VEC;
+    bool in[NV];
+    float dw[NV][VEC], dch[NV][VEC];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+        in[j] = p.c0 + j * dc < pl.W;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-            w[j][i] = (a.w && c < pl.W) ? __ldg(a.w + c + i) : 1.0f;
-            dw[j][i] = dc[j][i] = 0.0f;
-        }
-    for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += (int64_t)gridDim.x * pl.ty) {
-        const int64_t r = r0 + p.ty;
-        const bool on = r < a.rows;
-        float h[NV][VEC], dy[NV][VEC], s[2] = {0.0f, 0.0f};
+        for (int i = 0; i < VEC; ++i) dw[j][i] = dch[j][i] = 0.0f;
+    }
+    Raw<R, VEC> rh[NV], rd[NV];
+    Raw<T, VEC> ry[NV], rx[NV];
+    extern __shared__ __align__(128) unsigned char ring_smem[];
+    Ring<4> ring;
+    int st = 0;  // the row's stage, and its phase
+    uint32_t phase = 0;
+    auto refill = [&](int stage, int64_t row) {
+        const void *const src[4] = {static_cast<const R *>(a.res_out) + row * a.ro_sr, static_cast<const T *>(a.dy) + row * a.y_sr,
+                                     static_cast<const R *>(a.dres_out) + row * a.res_sr, static_cast<const T *>(a.x) + row * a.x_sr};
+        ring.issue(stage, src);
+    };
+    if constexpr (RING) {
+        ring.bytes[0] = pl.W * (uint32_t)sizeof(R);
+        ring.bytes[1] = pl.W * (uint32_t)sizeof(T);
+        ring.bytes[2] = a.dres_out ? ring.bytes[0] : 0u;
+        ring.bytes[3] = a.dcs ? ring.bytes[1] : 0u;
+        ring.init(ring_smem, pl.stages);
+        __syncthreads();
+        if (threadIdx.x == 0)
+            for (int i = 0; i < pl.stages; ++i)
+                if (blockIdx.x + i * dr < a.rows) refill(i, blockIdx.x + i * dr);
+    }
+    int64_t r = (int64_t)blockIdx.x * pl.ty + p.ty;
+    for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += dr, r += dr) {
+        float s[2] = {0.0f, 0.0f};
+        if constexpr (RING) ring.wait(st, phase, a.status);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) h[j][i] = dy[j][i] = 0.0f;
-            if (on && c < pl.W) {
-                load_vec<R, VEC>(static_cast<const R *>(a.res_out) + r * a.ro_sr + c, h[j]);
-                load_vec<T, VEC>(static_cast<const T *>(a.dy) + r * a.y_sr + c, dy[j]);
+            const bool on = in[j] && r < a.rows;
+            if constexpr (RING) {
+                const uint32_t at = (p.c0 + j * dc) * (uint32_t)sizeof(T), ar = (p.c0 + j * dc) * (uint32_t)sizeof(R);
+                rh[j].load_shared(ring.row(st, 0) + ar, on);
+                ry[j].load_shared(ring.row(st, 1) + at, on);
+                rd[j].load_shared(ring.row(st, 2) + ar, on && a.dres_out);
+                rx[j].load_shared(ring.row(st, 3) + at, on && a.dcs);
+                continue;
             }
+            rh[j].load(static_cast<const R *>(a.res_out) + r * a.ro_sr + col + j * dc, on);
+            ry[j].load(static_cast<const T *>(a.dy) + r * a.y_sr + col + j * dc, on);
+            rd[j].load(static_cast<const R *>(a.dres_out) + r * a.res_sr + col + j * dc, on && a.dres_out);
+            rx[j].load(static_cast<const T *>(a.x) + r * a.x_sr + col + j * dc, on && a.dcs);
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float h[VEC], y[VEC], w[VEC];
+            rh[j].get(h);
+            ry[j].get(y);
+            weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], w);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
-                s[0] = fmaf(h[j][i], h[j][i], s[0]);
-                s[1] = fmaf(dy[j][i] * w[j][i], h[j][i], s[1]);
+                s[0] = fmaf(h[i], h[i], s[0]);
+                s[1] = fmaf(y[i] * w[i], h[i], s[1]);
             }
         }
-        group_sum<2>(s, pl.tpr, sm);
+        group_sum<2>(s, pl.tpr, sm, turn);
+        if constexpr (RING) {
+            // every thread has read the row: its place is the next one's
+            if (threadIdx.x == 0 && r + pl.stages * dr < a.rows) refill(st, r + pl.stages * dr);
+            if (++st == pl.stages) st = 0, ++phase;
+        }
         const float inv = rsqrtf(fmaf(s[0], invW, a.eps));
         const float k = inv * inv * s[1] * invW;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = p.c0 + j * pl.tpr * VEC;
-            if (on && c < pl.W) {
-                float d[VEC], x[VEC];
-                if (a.dres_out) {
-                    load_vec<R, VEC>(static_cast<const R *>(a.dres_out) + r * a.res_sr + c, d);
-                } else {
+            float h[VEC], y[VEC], w[VEC], d[VEC], x[VEC], c[VEC];
+            rh[j].get(h);
+            ry[j].get(y);
+            rd[j].get(d);
+            rx[j].get(x);
+            weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], w);
+            weights<VEC>(a.cs ? a.cs + col + j * dc : nullptr, in[j], c);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) d[i] = 0.0f;
-                }
-                if (a.dcs) load_vec<T, VEC>(static_cast<const T *>(a.x) + r * a.x_sr + c, x);
+            for (int i = 0; i < VEC; ++i) {
+                d[i] += inv * fmaf(-k, h[i], y[i] * w[i]);
+                dw[j][i] = fmaf(y[i], h[i] * inv, dw[j][i]);
+                dch[j][i] = fmaf(a.scale * d[i], x[i], dch[j][i]);
+            }
+            if (in[j] && r < a.rows) {
+                if (a.dres) store_vec<R, VEC>(static_cast<R *>(a.dres) + r * a.width + col + j * dc, d);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    d[i] += inv * fmaf(-k, h[j][i], dy[j][i] * w[j][i]);
-                    dw[j][i] = fmaf(dy[j][i], h[j][i] * inv, dw[j][i]);
-                }
-                if (a.dres) store_vec<R, VEC>(static_cast<R *>(a.dres) + r * a.width + c, d);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    d[i] *= a.scale;
-                    if (a.dcs) dc[j][i] = fmaf(d[i], x[i], dc[j][i]);
-                    if (a.cs) d[i] *= __ldg(a.cs + c + i);
-                }
-                if (a.dx) store_vec<T, VEC>(static_cast<T *>(a.dx) + r * a.width + c, d);
+                for (int i = 0; i < VEC; ++i) d[i] *= a.scale * c[i];
+                if (a.dx) store_vec<T, VEC>(static_cast<T *>(a.dx) + r * a.width + col + j * dc, d);
             }
         }
     }
-    const int64_t prow = (int64_t)blockIdx.x * pl.ty + p.ty;
-    float *part = a.part;
+    const int64_t prow = (int64_t)blockIdx.x * pl.ty + p.ty, parts = (int64_t)gridDim.x * pl.ty;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = p.c0 + j * pl.tpr * VEC;
-        if (c < pl.W) {
-            if (a.dw) store_vec<float, VEC>(part + prow * a.width + c, dw[j]);
-            if (a.dcs) store_vec<float, VEC>(part + ((int64_t)gridDim.x * pl.ty + prow) * a.width + c, dc[j]);
-        }
+        if (!in[j]) continue;
+        if (a.dw) store_vec<float, VEC>(a.part + prow * a.width + col + j * dc, dw[j]);
+        if (a.dcs) store_vec<float, VEC>(a.part + (parts + prow) * a.width + col + j * dc, dch[j]);
     }
 }
 
@@ -404,11 +682,9 @@ int threads_for(int64_t W, int vec, int nv) {
     return t;
 }
 
-// Vectors per thread: the fewest that keep a group within a block, and for
-// groups of more than 256 vectors at least two, so that a block's sum over its
-// warps is paid by more bytes.
+// Vectors per thread: the fewest that keep a group within a block.
 int vectors_for(int64_t W, int vec) {
-    for (int nv = W > 256 * vec ? 2 : 1; nv < 32; nv *= 2)
+    for (int nv = 1; nv < 32; nv *= 2)
         if (threads_for(W, vec, nv) <= kMaxThr) return nv;
     return 32;
 }
@@ -431,32 +707,64 @@ NormPlan plan_norm(int64_t rows, int64_t W, int64_t groups, int vec, int nv, int
     }
     pl.gblocks = (int)((groups + pl.gb - 1) / pl.gb);
     const int64_t rb = (rows + pl.ty - 1) / pl.ty;
-    // the backward's partial sums are one row per block and ty: few blocks, each down many rows
-    const int64_t per_sm = std::max<int64_t>(1, (bwd ? 1024 : 2048) / ((int64_t)pl.tpr * pl.gb * pl.ty));
+    // as many blocks as run at a time (the backward leaves a row of partial sums per block and ty)
+    const int64_t thr = (int64_t)pl.tpr * pl.gb * pl.ty;
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(2048 / thr, 65536 / ((nv > 2 ? 128 : nv == 2 ? 96 : 64) * thr)));
     const int64_t cap = std::max<int64_t>(1, (int64_t)num_sms * per_sm / pl.gblocks);
     pl.rblocks = (int)std::max<int64_t>(1, std::min(rb, cap));
     return pl;
+}
+
+// A ring of rows pays where a block works down several of them and a group fills more than
+// a warp; its blocks share the SM's shared memory.
+constexpr int kMaxSmem = 220 * 1024;
+void add_ring(NormPlan &pl, int64_t rows, int vec, size_t row_bytes, int num_sms) {
+    if (vec == 1 || pl.tpr <= 32 || rows < 3 * (int64_t)pl.rblocks) return;
+    const int64_t per_sm = std::max<int64_t>(1, ((int64_t)pl.rblocks * pl.gblocks + num_sms - 1) / num_sms);
+    const int64_t n = (kMaxSmem / per_sm - 1024 - 128) / (int64_t)row_bytes;
+    pl.stages = (int)std::min<int64_t>(n, 8);
+    if (pl.stages < 2) pl.stages = 0;
 }
 
 bool vec16(const void *p, int64_t sr, int es) {
     return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (sr * es) % 16 == 0);
 }
 
-template <int NV, typename T, int VEC>
-cudaError_t run_gated(const GatedNormArgs &a, const NormPlan &pl, bool bwd, cudaStream_t st) {
-    const dim3 grid((unsigned)pl.rblocks, (unsigned)pl.gblocks);
-    const unsigned thr = (unsigned)(pl.tpr * pl.gb * pl.ty);
-    if (bwd) gated_norm_bwd_kernel<T, VEC, NV><<<grid, thr, 0, st>>>(a, pl);
-    else gated_norm_fwd_kernel<T, VEC, NV><<<grid, thr, 0, st>>>(a, pl);
+template <typename K, typename A>
+cudaError_t launch(K kernel, const A &a, const NormPlan &pl, size_t row_bytes, SmemOptIn &opt_in, cudaStream_t st) {
+    const size_t smem = pl.stages ? 128 + pl.stages * row_bytes : 0;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = opt_in.ensure(reinterpret_cast<const void *>(kernel), kMaxSmem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<dim3((unsigned)pl.rblocks, (unsigned)pl.gblocks), (unsigned)(pl.tpr * pl.gb * pl.ty), smem, st>>>(a, pl);
     return cudaGetLastError();
 }
+template <int NV, typename T, int VEC, int GATE>
+cudaError_t run_gate(const GatedNormArgs &a, const NormPlan &pl, size_t row_bytes, bool bwd, cudaStream_t st) {
+    static SmemOptIn opt_in[2];
+    if constexpr (VEC > 1)
+        if (pl.stages)
+            return bwd ? launch(gated_norm_bwd_kernel<T, VEC, NV, true, GATE>, a, pl, row_bytes, opt_in[1], st)
+                       : launch(gated_norm_fwd_kernel<T, VEC, NV, true, GATE>, a, pl, row_bytes, opt_in[0], st);
+    return bwd ? launch(gated_norm_bwd_kernel<T, VEC, NV, false, GATE>, a, pl, 0, opt_in[1], st)
+               : launch(gated_norm_fwd_kernel<T, VEC, NV, false, GATE>, a, pl, 0, opt_in[0], st);
+}
+template <int NV, typename T, int VEC>
+cudaError_t run_gated(const GatedNormArgs &a, const NormPlan &pl, size_t row_bytes, bool bwd, cudaStream_t st) {
+    if (!a.z) return run_gate<NV, T, VEC, kNoGate>(a, pl, row_bytes, bwd, st);
+    return a.gate_first ? run_gate<NV, T, VEC, kGateFirst>(a, pl, row_bytes, bwd, st)
+                        : run_gate<NV, T, VEC, kGateBehind>(a, pl, row_bytes, bwd, st);
+}
 template <int NV, typename T, typename R, int VEC>
-cudaError_t run_residual(const ResidualNormArgs &a, const NormPlan &pl, bool bwd, cudaStream_t st) {
-    const dim3 grid((unsigned)pl.rblocks, 1u);
-    const unsigned thr = (unsigned)(pl.tpr * pl.gb * pl.ty);
-    if (bwd) residual_norm_bwd_kernel<T, R, VEC, NV><<<grid, thr, 0, st>>>(a, pl);
-    else residual_norm_fwd_kernel<T, R, VEC, NV><<<grid, thr, 0, st>>>(a, pl);
-    return cudaGetLastError();
+cudaError_t run_residual(const ResidualNormArgs &a, const NormPlan &pl, size_t row_bytes, bool bwd, cudaStream_t st) {
+    static SmemOptIn opt_in[2];
+    if constexpr (VEC > 1)
+        if (pl.stages)
+            return bwd ? launch(residual_norm_bwd_kernel<T, R, VEC, NV, true>, a, pl, row_bytes, opt_in[1], st)
+                       : launch(residual_norm_fwd_kernel<T, R, VEC, NV, true>, a, pl, row_bytes, opt_in[0], st);
+    return bwd ? launch(residual_norm_bwd_kernel<T, R, VEC, NV, false>, a, pl, 0, opt_in[1], st)
+               : launch(residual_norm_fwd_kernel<T, R, VEC, NV, false>, a, pl, 0, opt_in[0], st);
 }
 
 cudaError_t sum_parts(const float *part, float *o0, float *o1, const NormPlan &pl, int64_t width, cudaStream_t st) {
@@ -496,17 +804,20 @@ cudaError_t launch_gated_norm(const GatedNormArgs &a, bool bf16, bool bwd, int n
     const int64_t W = a.width / a.groups;
     const int es = bf16 ? 2 : 4, v = bf16 ? 8 : 4;
     const bool ok = W % v == 0 && vec16(a.x, a.x_sr, es) && vec16(a.z, a.z_sr, es) && vec16(a.y, a.y_sr, es) &&
-                    vec16(a.dy, a.y_sr, es) && vec16(a.dx, a.width, es) && vec16(a.dz, a.width, es);
+                    vec16(a.dy, a.y_sr, es) && vec16(a.dx, a.width, es) && vec16(a.dz, a.width, es) && vec16(a.w, 0, 4);
     const int vec = ok ? v : 1, nv = vectors_for(W, vec);
-    const NormPlan pl = plan_norm(a.rows, W, a.groups, vec, nv, num_sms, bwd);
-    cudaError_t e = with_nv(nv, [&](auto n) {
+    NormPlan pl = plan_norm(a.rows, W, a.groups, vec, nv, num_sms, bwd);
+    const size_t rb = (size_t)W * es * ((bwd ? 2 : 1) + (a.z ? 1 : 0));
+    add_ring(pl, a.rows, vec, rb, num_sms);
+    cudaError_t e = with_nv(nv, [&](auto n) -> cudaError_t {
         constexpr int NV = decltype(n)::value;
         if (vec == 1)
-            return bf16 ? run_gated<NV, __nv_bfloat16, 1>(a, pl, bwd, stream) : run_gated<NV, float, 1>(a, pl, bwd, stream);
-        if constexpr (NV <= 8)
-            return bf16 ? run_gated<NV, __nv_bfloat16, 8>(a, pl, bwd, stream) : run_gated<NV, float, 4>(a, pl, bwd, stream);
-        else
-            return cudaErrorInvalidConfiguration;
+            return bf16 ? run_gated<NV, __nv_bfloat16, 1>(a, pl, rb, bwd, stream) : run_gated<NV, float, 1>(a, pl, rb, bwd, stream);
+        if constexpr (NV <= 8) {
+            if (!bf16) return run_gated<NV, float, 4>(a, pl, rb, bwd, stream);
+            if constexpr (NV <= 4) return run_gated<NV, __nv_bfloat16, 8>(a, pl, rb, bwd, stream);
+        }
+        return cudaErrorInvalidConfiguration;
     });
     if (e == cudaSuccess && bwd) e = sum_parts(a.part, a.dw, nullptr, pl, a.width, stream);
     return e;
@@ -518,24 +829,28 @@ cudaError_t launch_residual_norm(const ResidualNormArgs &a, bool bf16, bool res_
     const int es = bf16 ? 2 : 4, rs = res_bf16 ? 2 : 4, v = bf16 || res_bf16 ? 8 : 4;
     const bool ok = W % v == 0 && vec16(a.x, a.x_sr, es) && vec16(a.res, a.res_sr, rs) && vec16(a.y, a.y_sr, es) &&
                     vec16(a.dy, a.y_sr, es) && vec16(a.res_out, a.ro_sr, rs) && vec16(a.dres_out, a.res_sr, rs) &&
-                    vec16(a.dx, a.width, es) && vec16(a.dres, a.width, rs);
+                    vec16(a.dx, a.width, es) && vec16(a.dres, a.width, rs) && vec16(a.w, 0, 4) && vec16(a.cs, 0, 4);
     const int vec = ok ? v : 1, nv = vectors_for(W, vec);
-    const NormPlan pl = plan_norm(a.rows, W, 1, vec, nv, num_sms, bwd);
+    NormPlan pl = plan_norm(a.rows, W, 1, vec, nv, num_sms, bwd);
+    const size_t rb = (size_t)W * (bwd ? rs * (a.dres_out ? 2 : 1) + es * (a.dcs ? 2 : 1) : es + (a.res ? rs : 0));
+    add_ring(pl, a.rows, vec, rb, num_sms);
     cudaError_t e = with_nv(nv, [&](auto n) -> cudaError_t {
         constexpr int NV = decltype(n)::value;
         if (vec == 1) {
             if (bf16)
-                return res_bf16 ? run_residual<NV, __nv_bfloat16, __nv_bfloat16, 1>(a, pl, bwd, stream)
-                                : run_residual<NV, __nv_bfloat16, float, 1>(a, pl, bwd, stream);
-            return res_bf16 ? run_residual<NV, float, __nv_bfloat16, 1>(a, pl, bwd, stream)
-                            : run_residual<NV, float, float, 1>(a, pl, bwd, stream);
+                return res_bf16 ? run_residual<NV, __nv_bfloat16, __nv_bfloat16, 1>(a, pl, rb, bwd, stream)
+                                : run_residual<NV, __nv_bfloat16, float, 1>(a, pl, rb, bwd, stream);
+            return res_bf16 ? run_residual<NV, float, __nv_bfloat16, 1>(a, pl, rb, bwd, stream)
+                            : run_residual<NV, float, float, 1>(a, pl, rb, bwd, stream);
         }
         if constexpr (NV <= 8) {
-            if (bf16)
-                return res_bf16 ? run_residual<NV, __nv_bfloat16, __nv_bfloat16, 8>(a, pl, bwd, stream)
-                                : run_residual<NV, __nv_bfloat16, float, 8>(a, pl, bwd, stream);
-            return res_bf16 ? run_residual<NV, float, __nv_bfloat16, 8>(a, pl, bwd, stream)
-                            : run_residual<NV, float, float, 4>(a, pl, bwd, stream);
+            if (vec == 4) return run_residual<NV, float, float, 4>(a, pl, rb, bwd, stream);
+            if constexpr (NV <= 4) {
+                if (bf16)
+                    return res_bf16 ? run_residual<NV, __nv_bfloat16, __nv_bfloat16, 8>(a, pl, rb, bwd, stream)
+                                    : run_residual<NV, __nv_bfloat16, float, 8>(a, pl, rb, bwd, stream);
+                return run_residual<NV, float, __nv_bfloat16, 8>(a, pl, rb, bwd, stream);
+            }
         }
         return cudaErrorInvalidConfiguration;
     });

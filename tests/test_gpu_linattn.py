@@ -295,7 +295,8 @@ def test_same_bits_over_many_runs(b, L, H, G, dk, dv):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("b,H,G,dk,dv", [(1, 1, 1, 1, 1), (3, 4, 2, 64, 64), (2, 8, 1, 128, 64), (2, 3, 3, 40, 72),
-                                         (2, 2, 1, 7, 5), (1, 2, 2, 300, 256), (5, 6, 3, 16, 128), (2, 2, 2, 128, 130)])
+                                         (2, 2, 1, 7, 5), (1, 2, 2, 300, 256), (5, 6, 3, 16, 128), (2, 2, 2, 128, 130),
+                                         (1, 2, 1, 300, 4), (2, 1, 1, 700, 16), (1, 1, 1, 513, 1)])
 def test_step(dtype, b, H, G, dk, dv):
     x = make(b, H, G, dk, dv, dtype, b * dk + dv, n=b)
     st = x["s0"].to(DEV)
