@@ -694,30 +694,37 @@ def state_update(state, x, delta, A, B, C, D=None, z=None, delta_bias=None, soft
 
 # ------------------------------------------- linear attention and its norms ----
 
+_cuda = None  # torch's own entry points for the current device and stream, looked up once
+
+
 def _layer_call(ref, stream, *others):
     """The stream handle for a call on ``ref``'s device, every tensor checked
     to be on that device and the device to be the current one (the library
     launches on the current device)."""
-    torch = _torch()
-    dev = ref.device
-    if dev.type != "cuda":
+    global _cuda
+    dev = ref.get_device()
+    if dev < 0:
         raise ValueError("expected CUDA tensors")
     for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but cuda:{torch.cuda.current_device()} is the current device")
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {ref.device} and {t.device}")
+    if _cuda is None:
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _cuda = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                 raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+    if dev != _cuda[0]():
+        raise ValueError(f"tensors on {ref.device}, but cuda:{_cuda[0]()} is the current device")
+    return _cuda[1](dev) if stream is None else stream.cuda_stream
 
 
 def _same_type(t, shape, dtype, name):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype or (t.numel() > 0 and t.stride(-1) != 1)):
+    if t is not None and (t.shape != shape or t.dtype != dtype or (t.stride(-1) != 1 and t.numel() > 0)):
         raise ValueError(f"{name} must be {tuple(shape)} {dtype} with unit stride along its last dimension")
 
 
 def _dense_f32(t, shape, name):
-    torch = _torch()
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != torch.float32 or not t.is_contiguous()):
+    if t is not None and (t.shape != shape or t.dtype != _torch().float32 or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {tuple(shape)}")
 
 
@@ -773,15 +780,14 @@ def linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, seq_start=Non
     ``final_state`` may be ``initial_state``. ``workspace`` (uint8 CUDA tensor
     of at least ``mamba_linattn_workspace_size`` bytes) is allocated per call
     when omitted. Returns (o, final_state or None)."""
-    torch = _torch()
     n, H, dk, dv, oshape = _check_linattn(q, k, v, log_decay, seq_start)
     if o is None:
-        o = torch.empty(oshape, dtype=q.dtype, device=q.device)
+        o = q.new_empty(oshape)
     else:
         _same_type(o, oshape, q.dtype, "o")
     fs = final_state
     if fs is None and return_final_state:
-        fs = torch.empty((n, H, dk, dv), dtype=torch.float32, device=q.device)
+        fs = log_decay.new_empty((n, H, dk, dv))
     _dense_f32(initial_state, (n, H, dk, dv), "initial_state")
     _dense_f32(final_state, (n, H, dk, dv), "final_state")
     st = _layer_call(q, stream, k, v, log_decay, seq_start, initial_state, o, fs, dev_status, workspace)
@@ -831,21 +837,21 @@ def linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] = Non
     """One token of linattn_fwd: state [b, H, dk, dv] fp32 (dense [dk, dv]
     blocks, updated in place), q [b, H, dk], k [b, G, dk], v [b, G, dv].
     Returns o [b, H, dv]."""
-    torch = _torch()
     b, H, dk = q.shape
     G, dv = v.shape[1], v.shape[2]
-    if state.shape != (b, H, dk, dv) or state.dtype != torch.float32 or state.stride()[2:] != (dv, 1):
+    ss = state.stride()
+    if state.shape != (b, H, dk, dv) or state.dtype != _torch().float32 or ss[2:] != (dv, 1):
         raise ValueError(f"state must be {(b, H, dk, dv)} fp32 with dense [dk, dv] blocks")
     _same_type(q, q.shape, q.dtype, "q")
     _same_type(k, (b, G, dk), q.dtype, "k")
     _same_type(v, (b, G, dv), q.dtype, "v")
     _dense_f32(log_decay, (H,), "log_decay")
     if o is None:
-        o = torch.empty((b, H, dv), dtype=q.dtype, device=q.device)
+        o = q.new_empty((b, H, dv))
     else:
         _same_type(o, (b, H, dv), q.dtype, "o")
     st = _layer_call(state, stream, q, k, v, log_decay, o, dev_status)
-    qs, ks, vs, os_, ss = q.stride(), k.stride(), v.stride(), o.stride(), state.stride()
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
     dims = LinattnUpdateDims(b, H, G, dk, dv, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], ss[0], ss[1],
                              _dtype_code(q))
     rc = mamba_linattn_state_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
@@ -855,13 +861,13 @@ def linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] = Non
     return o
 
 
-def _rows(t, name, shape=None, dtype=None):
+def _rows(t, name, shape, dtype):
+    """The row stride of a [rows, width] tensor, 0 for none."""
     if t is None:
         return 0
-    if t.dim() != 2:
+    if len(shape) != 2:
         raise ValueError(f"{name} must be [rows, width]")
-    if shape is not None:
-        _same_type(t, shape, dtype, name)
+    _same_type(t, shape, dtype, name)
     return t.stride(0)
 
 
@@ -870,12 +876,11 @@ def gated_norm_fwd(x, z=None, weight=None, groups: int = 1, eps: float = 1e-5, g
     """Gated group norm (see include/mambascan.h, mamba_gated_norm_fwd) of x
     [rows, width]: norm(x) w silu(z), or norm(x silu(z)) w with
     ``gate_first``. Returns y."""
-    torch = _torch()
     xs = _rows(x, "x", x.shape, x.dtype)
     zs = _rows(z, "z", x.shape, x.dtype)
     _dense_f32(weight, x.shape[1:], "weight")
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        y = x.new_empty(x.shape)
     st = _layer_call(x, stream, z, weight, y, dev_status)
     dims = GatedNormDims(x.shape[0], x.shape[1], groups, xs, zs, _rows(y, "y", x.shape, x.dtype), eps, _dtype_code(x),
                          int(gate_first))
@@ -914,19 +919,19 @@ def residual_norm_fwd(x, residual=None, weight=None, eps: float = 1e-5, res_scal
     channel_scale x, y = norm(residual_out) weight. ``residual_out`` (of the
     residual's type, else of ``residual_dtype``, else x's) may be
     ``residual``. Returns (y, residual_out)."""
-    torch = _torch()
-    xs = _rows(x, "x", x.shape, x.dtype)
+    shape = x.shape
+    xs = _rows(x, "x", shape, x.dtype)
     rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else \
         residual_dtype or x.dtype
     if residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=rt, device=x.device)
+        residual_out = x.new_empty(shape, dtype=rt)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _dense_f32(weight, x.shape[1:], "weight")
-    _dense_f32(channel_scale, x.shape[1:], "channel_scale")
+        y = x.new_empty(shape)
+    _dense_f32(weight, shape[1:], "weight")
+    _dense_f32(channel_scale, shape[1:], "channel_scale")
     st = _layer_call(x, stream, residual, weight, channel_scale, y, residual_out, dev_status)
-    dims = ResidualNormDims(x.shape[0], x.shape[1], xs, _rows(residual, "residual", x.shape, rt),
-                            _rows(y, "y", x.shape, x.dtype), _rows(residual_out, "residual_out", x.shape, rt), eps,
+    dims = ResidualNormDims(shape[0], shape[1], xs, _rows(residual, "residual", shape, rt),
+                            _rows(y, "y", shape, x.dtype), _rows(residual_out, "residual_out", shape, rt), eps,
                             res_scale, _dtype_code(x), _dtype_code(residual_out))
     rc = mamba_residual_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(channel_scale), _ptr(y),
                                  _ptr(residual_out), dims, _ptr(dev_status), st)

@@ -29,11 +29,10 @@ namespace ms {
 
 namespace {
 
-constexpr int kMaxThr = 512;  // threads of a block, at most
-// Registers of a thread: with 96, blocks of 320 threads (5120 bf16 columns) run two to an
-// SM and have 60 KB of rows on their way; the wider rows' threads hold more of them.
-template <int NV>
-constexpr int kRegs = NV <= 1 ? 64 : NV <= 2 ? 96 : 128;
+constexpr int kMaxThr = 640;  // threads of a block, at most
+// Registers of a thread. The backward keeps its columns' weights and their sums; its
+// blocks of 640 threads (5120 bf16 columns) run one to an SM, of 320 two.
+constexpr int regs_of(int nv, bool bwd) { return nv > 1 || bwd ? 96 : 56; }
 
 // VEC neighbouring elements as they lie in memory: a row waits in this form.
 template <typename T, int VEC>
@@ -227,6 +226,10 @@ __device__ __forceinline__ Place place_of(const NormPlan &pl, int64_t groups) {
     return p;
 }
 
+// Weights of a thread's columns: read once where they fit into registers, else for every row (from L1).
+template <int VEC, int NV>
+constexpr bool kHold = VEC *NV <= 8;
+
 // How the gate takes part: not at all, behind the norm, or in front of it.
 enum { kNoGate = 0, kGateBehind = 1, kGateFirst = 2 };
 __device__ __forceinline__ float sigmoid_f(float z) { return rcp_mufu(1.0f + exp2_mufu(-z * kLog2e)); }
@@ -237,7 +240,7 @@ template <int VEC, int NV, bool RING>
 constexpr bool kAhead = !RING && VEC *NV <= 16;
 
 template <typename T, int VEC, int NV, bool RING, int GATE>
-__global__ void __maxnreg__(kRegs<NV>) gated_norm_fwd_kernel(const GatedNormArgs a, const NormPlan pl) {
+__global__ void __maxnreg__(regs_of(NV, false)) gated_norm_fwd_kernel(const GatedNormArgs a, const NormPlan pl) {
     __shared__ float sm[2][2 * kMaxWarps];
     int turn = 0;
     const Place p = place_of<VEC>(pl, a.groups);
@@ -328,7 +331,7 @@ __global__ void __maxnreg__(kRegs<NV>) gated_norm_fwd_kernel(const GatedNormArgs
 }
 
 template <typename T, int VEC, int NV, bool RING, int GATE>
-__global__ void __maxnreg__(kRegs<NV>) gated_norm_bwd_kernel(const GatedNormArgs a, const NormPlan pl) {
+__global__ void __maxnreg__(regs_of(NV, true)) gated_norm_bwd_kernel(const GatedNormArgs a, const NormPlan pl) {
     __shared__ float sm[2][2 * kMaxWarps];
     int turn = 0;
     const Place p = place_of<VEC>(pl, a.groups);
@@ -346,7 +349,19 @@ __global__ void __maxnreg__(kRegs<NV>) gated_norm_bwd_kernel(const GatedNormArgs
     Raw<T, VEC> rx[NV], rz[NV], ry[NV];
     const T *x = static_cast<const T *>(a.x) + col, *z = static_cast<const T *>(a.z) + col;
     const T *dy = static_cast<const T *>(a.dy) + col;
-    const float *wt = a.w ? a.w + col : nullptr;  // read again for every row (it stays in L1)
+    const float *wt = a.w ? a.w + col : nullptr;
+    float hw[kHold<VEC, NV> ? NV : 1][VEC];
+    if constexpr (kHold<VEC, NV>)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) weights<VEC>(wt ? wt + j * dc : nullptr, in[j], hw[j]);
+    auto weights_of = [&](int j, float (&w)[VEC]) {
+        if constexpr (kHold<VEC, NV>) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = hw[j][i];
+        } else {
+            weights<VEC>(wt ? wt + j * dc : nullptr, in[j], w);
+        }
+    };
     extern __shared__ __align__(128) unsigned char ring_smem[];
     Ring<3> ring;
     int st = 0;  // the row's stage, and its phase
@@ -391,7 +406,7 @@ __global__ void __maxnreg__(kRegs<NV>) gated_norm_bwd_kernel(const GatedNormArgs
             float u[VEC], gr[VEC], z_[VEC], w[VEC];
             rx[j].get(u);
             ry[j].get(gr);
-            weights<VEC>(wt ? wt + j * dc : nullptr, in[j], w);
+            weights_of(j, w);
             if constexpr (GATE != kNoGate) {
                 rz[j].get(z_);
 #pragma unroll
@@ -420,7 +435,7 @@ __global__ void __maxnreg__(kRegs<NV>) gated_norm_bwd_kernel(const GatedNormArgs
             float u[VEC], gr[VEC], z_[VEC], w[VEC], dz[VEC];
             rx[j].get(u);
             ry[j].get(gr);
-            weights<VEC>(wt ? wt + j * dc : nullptr, in[j], w);
+            weights_of(j, w);
             if constexpr (GATE != kNoGate) rz[j].get(z_);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
@@ -458,7 +473,7 @@ __global__ void __maxnreg__(kRegs<NV>) gated_norm_bwd_kernel(const GatedNormArgs
 }
 
 template <typename T, typename R, int VEC, int NV, bool RING>
-__global__ void __maxnreg__(kRegs<NV>) residual_norm_fwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
+__global__ void __maxnreg__(regs_of(NV, false)) residual_norm_fwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
     __shared__ float sm[2][2 * kMaxWarps];
     int turn = 0;
     const Place p = place_of<VEC>(pl, 1);
@@ -543,7 +558,7 @@ __global__ void __maxnreg__(kRegs<NV>) residual_norm_fwd_kernel(const ResidualNo
 }
 
 template <typename T, typename R, int VEC, int NV, bool RING>
-__global__ void __maxnreg__(kRegs<NV>) residual_norm_bwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
+__global__ void __maxnreg__(regs_of(NV, true)) residual_norm_bwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
     __shared__ float sm[2][2 * kMaxWarps];
     int turn = 0;
     const Place p = place_of<VEC>(pl, 1);
@@ -558,6 +573,21 @@ __global__ void __maxnreg__(kRegs<NV>) residual_norm_bwd_kernel(const ResidualNo
 #pragma unroll
         for (int i = 0; i < VEC; ++i) dw[j][i] = dch[j][i] = 0.0f;
     }
+    float hw[kHold<VEC, NV> ? NV : 1][VEC], hc[kHold<VEC, NV> ? NV : 1][VEC];
+    if constexpr (kHold<VEC, NV>)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], hw[j]);
+            weights<VEC>(a.cs ? a.cs + col + j * dc : nullptr, in[j], hc[j]);
+        }
+    auto weights_of = [&](const float *from, const float (&held)[kHold<VEC, NV> ? NV : 1][VEC], int j, float (&w)[VEC]) {
+        if constexpr (kHold<VEC, NV>) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) w[i] = held[j][i];
+        } else {
+            weights<VEC>(from ? from + col + j * dc : nullptr, in[j], w);
+        }
+    };
     Raw<R, VEC> rh[NV], rd[NV];
     Raw<T, VEC> ry[NV], rx[NV];
     extern __shared__ __align__(128) unsigned char ring_smem[];
@@ -605,7 +635,7 @@ __global__ void __maxnreg__(kRegs<NV>) residual_norm_bwd_kernel(const ResidualNo
             float h[VEC], y[VEC], w[VEC];
             rh[j].get(h);
             ry[j].get(y);
-            weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], w);
+            weights_of(a.w, hw, j, w);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 s[0] = fmaf(h[i], h[i], s[0]);
@@ -627,8 +657,8 @@ __global__ void __maxnreg__(kRegs<NV>) residual_norm_bwd_kernel(const ResidualNo
             ry[j].get(y);
             rd[j].get(d);
             rx[j].get(x);
-            weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], w);
-            weights<VEC>(a.cs ? a.cs + col + j * dc : nullptr, in[j], c);
+            weights_of(a.w, hw, j, w);
+            weights_of(a.cs, hc, j, c);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 d[i] += inv * fmaf(-k, h[i], y[i] * w[i]);
@@ -652,23 +682,26 @@ __global__ void __maxnreg__(kRegs<NV>) residual_norm_bwd_kernel(const ResidualNo
     }
 }
 
-// out[c] = sum over the rows of part, each thread its own rows in order and
-// then the threads of a column in order.
-__global__ void __launch_bounds__(256) norm_sum_kernel(const float *part, float *out0, float *out1, int64_t parts,
-                                                       int64_t width) {
-    __shared__ float sm[8][32];
+// out[c] = sum over the rows of part, each thread its own rows in order and then
+// the threads of a column in order. Latency bounds it: 32 threads share a column.
+constexpr int kSumRows = 32;
+__global__ void __launch_bounds__(32 * kSumRows) norm_sum_kernel(const float *part, float *out0, float *out1, int64_t parts,
+                                                                 int64_t width) {
+    __shared__ float sm[kSumRows][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + tx;
     float *out = blockIdx.y ? out1 : out0;
     if (out == nullptr) return;
     const float *src = part + (int64_t)blockIdx.y * parts * width;
     float s = 0.0f;
-    if (c < width)
-        for (int64_t r = ty; r < parts; r += 8) s += src[r * width + c];
+    if (c < width) {
+#pragma unroll 8
+        for (int64_t r = ty; r < parts; r += kSumRows) s += src[r * width + c];
+    }
     sm[ty][tx] = s;
     __syncthreads();
     if (ty == 0 && c < width) {
-        for (int i = 1; i < 8; ++i) s += sm[i][tx];
+        for (int i = 1; i < kSumRows; ++i) s += sm[i][tx];
         out[c] = s;
     }
 }
@@ -709,7 +742,7 @@ NormPlan plan_norm(int64_t rows, int64_t W, int64_t groups, int vec, int nv, int
     const int64_t rb = (rows + pl.ty - 1) / pl.ty;
     // as many blocks as run at a time (the backward leaves a row of partial sums per block and ty)
     const int64_t thr = (int64_t)pl.tpr * pl.gb * pl.ty;
-    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(2048 / thr, 65536 / ((nv > 2 ? 128 : nv == 2 ? 96 : 64) * thr)));
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(2048 / thr, 65536 / (regs_of(nv, bwd) * thr)));
     const int64_t cap = std::max<int64_t>(1, (int64_t)num_sms * per_sm / pl.gblocks);
     pl.rblocks = (int)std::max<int64_t>(1, std::min(rb, cap));
     return pl;
@@ -769,8 +802,8 @@ cudaError_t run_residual(const ResidualNormArgs &a, const NormPlan &pl, size_t r
 
 cudaError_t sum_parts(const float *part, float *o0, float *o1, const NormPlan &pl, int64_t width, cudaStream_t st) {
     if (!o0 && !o1) return cudaSuccess;
-    const dim3 grid((unsigned)((width + 31) / 32), 2u);
-    norm_sum_kernel<<<grid, 256, 0, st>>>(part, o0, o1, (int64_t)pl.rblocks * pl.ty, width);
+    const dim3 grid((unsigned)((width + 31) / 32), o1 ? 2u : 1u);
+    norm_sum_kernel<<<grid, 32 * kSumRows, 0, st>>>(part, o0, o1, (int64_t)pl.rblocks * pl.ty, width);
     return cudaGetLastError();
 }
 
