@@ -212,10 +212,10 @@ int mamba_linattn_bwd(const void *q, const void *k, const void *v, const float *
         r.batch = d->batch; r.seqlen = d->seqlen; r.total = d->total; r.H = d->nheads; r.kv = d->kv_heads;
         r.part = reinterpret_cast<const float *>(ws);
         r.out = dk_; r.d = dk; r.o_sb = d->k_sb; r.o_sl = d->k_sl; r.o_sh = d->k_sh;
-        e = ms::launch_linattn_reduce(r, bf16, st);
-        r.part = reinterpret_cast<const float *>(ws + pk);
-        r.out = dv_; r.d = dv; r.o_sb = d->v_sb; r.o_sl = d->v_sl; r.o_sh = d->v_sh;
-        if (e == cudaSuccess) e = ms::launch_linattn_reduce(r, bf16, st);
+        ms::LaReduceArgs r2 = r;
+        r2.part = reinterpret_cast<const float *>(ws + pk);
+        r2.out = dv_; r2.d = dv; r2.o_sb = d->v_sb; r2.o_sl = d->v_sl; r2.o_sh = d->v_sh;
+        e = ms::launch_linattn_reduce(r, r2, bf16, st);
     }
     return cuda_rc(e);
 }

@@ -123,23 +123,47 @@ cudaError_t launch_plain_t(const LaArgs &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-// out[row][g][i] = sum of part[row][h][i] over the heads h of g, in their order.
-template <typename T>
-__global__ void __launch_bounds__(256) linattn_reduce_kernel(const LaReduceArgs a) {
-    const int64_t per = a.kv * a.d, n = a.H / a.kv;
+// out[row][g][i] = sum of part[row][h][i] over the heads h of g, in their order, for
+// two arrays (blockIdx.y). HBM bounds it: a thread has VEC neighbouring columns of a
+// row (16 bytes of part), a block whole rows, and all heads' loads are on their way
+// together (4001 x 2 rows of 16 heads for 4, 128 and 96 columns: NNN us, 67 us with
+// one column a thread).
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256) linattn_reduce_kernel(const LaReduceArgs a0, const LaReduceArgs a1) {
+    const LaReduceArgs &a = blockIdx.y ? a1 : a0;
+    const int per = (int)(a.kv * a.d) / VEC, n = (int)(a.H / a.kv), dv = (int)a.d / VEC;
+    const int tpr = per < 256 ? per : 256, rpb = 256 / tpr;
+    const int x = threadIdx.x % tpr, y = threadIdx.x / tpr;
+    if (y >= rpb) return;
     int64_t first = 0, rows = a.batch * a.seqlen;
     if (a.seq_start) {
         const int64_t s = a.seq_start[0], e = a.seq_start[a.batch];
         first = s < 0 ? 0 : s;
         rows = (e < a.total ? e : a.total) - first;
     }
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = first + i / per, g = i % per / a.d, c = i % a.d;
-        const float *src = a.part + (row * a.H + g * n) * a.d + c;
-        float s = 0.0f;
-        for (int64_t j = 0; j < n; ++j) s += src[j * a.d];
-        const int64_t b = a.seq_start ? 0 : row / a.seqlen, t = a.seq_start ? row : row % a.seqlen;
-        Elem<T>::store(static_cast<T *>(a.out) + b * a.o_sb + t * a.o_sl + g * a.o_sh + c, s);
+    for (int64_t r = (int64_t)blockIdx.x * rpb + y; r < rows; r += (int64_t)gridDim.x * rpb) {
+        const int64_t row = first + r;
+        const int64_t b = a.seq_start ? 0 : row / a.seqlen, t = a.seq_start ? row : row - b * a.seqlen;
+        T *out = static_cast<T *>(a.out) + b * a.o_sb + t * a.o_sl;
+        const float *part = a.part + row * a.H * a.d;
+        for (int i = x; i < per; i += tpr) {
+            const int g = i / dv, c = (i - g * dv) * VEC;
+            const float *src = part + (int64_t)g * n * a.d + c;
+            float s[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) s[j] = 0.0f;
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                if constexpr (VEC == 4) {
+                    const float4 v = __ldcs(reinterpret_cast<const float4 *>(src + k * a.d));
+                    s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+                } else {
+                    s[0] += src[k * a.d];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) Elem<T>::store(out + g * a.o_sh + c + j, s[j]);
+        }
     }
 }
 
@@ -257,13 +281,19 @@ cudaError_t launch_linattn_plain(const LaArgs &a, bool bf16, cudaStream_t stream
     return bf16 ? launch_plain_t<__nv_bfloat16>(a, stream) : launch_plain_t<float>(a, stream);
 }
 
-cudaError_t launch_linattn_reduce(const LaReduceArgs &a, bool bf16, cudaStream_t stream) {
-    const int64_t n = (a.seq_start ? a.total : a.batch * a.seqlen) * a.kv * a.d;
-    if (n <= 0) return cudaSuccess;
-    const int64_t want = (n + 255) / 256;
-    const unsigned grid = (unsigned)(want < 148 * 16 ? want : 148 * 16);
-    if (bf16) linattn_reduce_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a);
-    else linattn_reduce_kernel<float><<<grid, 256, 0, stream>>>(a);
+cudaError_t launch_linattn_reduce(const LaReduceArgs &a, const LaReduceArgs &b, bool bf16, cudaStream_t stream) {
+    const int64_t rows = a.seq_start ? a.total : a.batch * a.seqlen;
+    if (rows <= 0) return cudaSuccess;
+    const dim3 grid((unsigned)(rows < 148 * 8 ? rows : 148 * 8), 2u);
+    const bool vec = a.d % 4 == 0 && b.d % 4 == 0 && reinterpret_cast<uintptr_t>(a.part) % 16 == 0 &&
+                     reinterpret_cast<uintptr_t>(b.part) % 16 == 0;
+    if (bf16) {
+        if (vec) linattn_reduce_kernel<__nv_bfloat16, 4><<<grid, 256, 0, stream>>>(a, b);
+        else linattn_reduce_kernel<__nv_bfloat16, 1><<<grid, 256, 0, stream>>>(a, b);
+    } else {
+        if (vec) linattn_reduce_kernel<float, 4><<<grid, 256, 0, stream>>>(a, b);
+        else linattn_reduce_kernel<float, 1><<<grid, 256, 0, stream>>>(a, b);
+    }
     return cudaGetLastError();
 }
 

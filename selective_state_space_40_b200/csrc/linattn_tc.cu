@@ -882,6 +882,16 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
                 auto add = [&](const float *from, int64_t sr, int64_t sc, float decay) {
                     const bool in = from && row < p.dx;
                     const int64_t at = row * sr + col0 * sc;
+                    if (sc == 1) {  // (and 16-byte aligned: dz is a multiple of 8)
+#pragma unroll
+                        for (int i = 0; i < NCOL; i += 4) {
+                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (in && col0 + i < p.dz) v = *reinterpret_cast<const float4 *>(from + at + i);
+                            S[i / 2] = f2_fma(f2_splat(decay), S[i / 2], f2_make(v.x, v.y));
+                            S[i / 2 + 1] = f2_fma(f2_splat(decay), S[i / 2 + 1], f2_make(v.z, v.w));
+                        }
+                        return;
+                    }
 #pragma unroll
                     for (int i = 0; i < NCOL; i += 2) {
                         const bool use = in && col0 + i < p.dz;  // (dz is a multiple of 8)
@@ -1115,7 +1125,7 @@ bool linattn_tc_applies(const LaArgs &a, bool bf16) {
         const int eo = p.o_f32 ? 4 : 2;
         if (p.dx % 8 || p.dz % 8 || !map_ok(key_x(a, p), batch) || !map_ok(key_y(a, p), batch) ||
             !map_ok(key_z(a, p), batch) || reinterpret_cast<uintptr_t>(p.o) % 16 || (p.o_sb * eo) % 16 ||
-            (p.o_sl * eo) % 16 || (p.o_sh * eo) % 16 || reinterpret_cast<uintptr_t>(p.fin) % 16)
+            (p.o_sl * eo) % 16 || (p.o_sh * eo) % 16 || reinterpret_cast<uintptr_t>(p.fin) % 16 || reinterpret_cast<uintptr_t>(p.s0) % 16)
             return false;
     }
     return true;

@@ -167,7 +167,7 @@ bool linattn_tc_applies(const LaArgs &a, bool bf16);
 size_t linattn_tc_workspace(int64_t batch, int64_t rows, bool packed, int64_t H, int dk, int dv, bool bwd, int num_sms);
 cudaError_t launch_linattn_tc(const LaArgs &a, void *workspace, int num_sms, cudaStream_t stream);
 // Sums the fp32 rows part [rows, H, d] over the H / kv heads that share a kv
-// head into out [row, kv, d] (rows as the problem's tokens lie).
+// head into out [row, kv, d] (rows as the problem's tokens lie), for two arrays.
 struct LaReduceArgs {
     const float *part;
     void *out;
@@ -175,7 +175,7 @@ struct LaReduceArgs {
     int64_t batch, seqlen, total, H, kv, d;
     int64_t o_sb, o_sl, o_sh;
 };
-cudaError_t launch_linattn_reduce(const LaReduceArgs &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_linattn_reduce(const LaReduceArgs &a, const LaReduceArgs &b, bool bf16, cudaStream_t stream);
 
 struct LaUpdateArgs {
     float *state;
