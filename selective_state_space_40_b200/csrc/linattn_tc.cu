@@ -126,7 +126,9 @@ struct Smem {
     static constexpr int kStages = DX == 64 ? 3 : 2;
     static constexpr int oZs = kStages * kStage;               // three parts of Z'
     static constexpr int oS = oZs + 3 * kZb;                   // S in bf16
-    static constexpr int oItem = oS + (kOwn ? 0 : DX * kZ * 2);  // two items
+    // states on their way, a part per warp of group S: at dx = 128 the warp's own rows of the S tile
+    static constexpr int oMove = DX == 64 ? oS + DX * kZ * 2 : oS;
+    static constexpr int oItem = oMove + DX * kZ * 2;          // two items
     // two items' tables: lam^n, n = 0..128; lam^|d| at 31 + d, d = t - s, 0 on the masked side;
     // lam^(31-c), in reverse lam^c, c < 32
     static constexpr int oTab = oItem + 2 * (int)sizeof(Item);
@@ -867,6 +869,15 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
         const uint32_t kv = tmem + ((uint32_t)(32 * w) << 16) + kColKv + (uint32_t)c0;
         const uint32_t dst = sbase + M::oS + 128u * row;
         const int x8 = row & 7, j0 = c0 >> 3;
+        // A thread holds a row (or half of one); states come and go through a part of shared memory
+        // that is the warp's own, kPc columns at a time, so that memory sees whole 64- or 128-byte pieces of kPr rows
+        // (rows straight to and from memory took 30 % of the packed batch's time).
+        constexpr int kPc = DX == 64 ? 16 : 32, kPr = 128 / kPc;
+        const int row0 = row - lane, pq = lane % (kPc / 4), pr = lane / (kPc / 4);
+        const uint32_t pbase = sbase + M::oMove + (uint32_t)(w * 32 * kPc * 4);
+        auto piece = [&](int r, int q) {
+            return pbase + (uint32_t)(r * kPc * 4 + ((q ^ (DX == 64 ? (r >> 1) & 3 : r & 7)) << 4));
+        };
         each_item([&](const Item &it, const float *tab) {
             const TcProblem &p = a.p[it.pi];
             const bool rev = p.rev != 0;
@@ -878,27 +889,7 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
 #pragma unroll
             for (int i = 0; i < NCOL / 2; ++i) S[i] = f2_splat(0.0f);
             if constexpr (!kOwn) {
-                // decay * S + an array's block
-                auto add = [&](const float *from, int64_t sr, int64_t sc, float decay) {
-                    const bool in = from && row < p.dx;
-                    const int64_t at = row * sr + col0 * sc;
-                    if (sc == 1) {  // (and 16-byte aligned: dz is a multiple of 8)
-#pragma unroll
-                        for (int i = 0; i < NCOL; i += 4) {
-                            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                            if (in && col0 + i < p.dz) v = *reinterpret_cast<const float4 *>(from + at + i);
-                            S[i / 2] = f2_fma(f2_splat(decay), S[i / 2], f2_make(v.x, v.y));
-                            S[i / 2 + 1] = f2_fma(f2_splat(decay), S[i / 2 + 1], f2_make(v.z, v.w));
-                        }
-                        return;
-                    }
-#pragma unroll
-                    for (int i = 0; i < NCOL; i += 2) {
-                        const bool use = in && col0 + i < p.dz;  // (dz is a multiple of 8)
-                        const float u = use ? from[at + i * sc] : 0.0f, v = use ? from[at + (i + 1) * sc] : 0.0f;
-                        S[i / 2] = f2_fma(f2_splat(decay), S[i / 2], f2_make(u, v));
-                    }
-                };
+                if (DX == 128 && cc > 0 && !wait_all(kBarOB, cc - 1)) return false;  // (the S tile is not read any more)
                 if (kMode == kChained && it.j > 0) {
                     // from the previous segment's item, once its four warps have handed it on
                     bool there = true;
@@ -914,22 +905,72 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
                         }
                     }
                     if (!__shfl_sync(0xffffffffu, there, 0)) return false;
-                    const float4 *from = reinterpret_cast<const float4 *>(a.chain + ((int64_t)chain * DX + row) * kZ + c0);
+                    // (laid out as the threads hold it: 4 columns of all rows)
+                    const float4 *from = reinterpret_cast<const float4 *>(a.chain) + ((int64_t)chain * (kZ / 4) + c0 / 4) * DX + row;
 #pragma unroll
                     for (int i = 0; i < NCOL; i += 4) {
-                        const float4 v = __ldcg(from + i / 4);
+                        const float4 v = __ldcg(from + (i / 4) * DX);
                         S[i / 2] = f2_make(v.x, v.y);
                         S[i / 2 + 1] = f2_make(v.z, v.w);
                     }
                 } else {
-                    add(p.s0 ? p.s0 + it.seq * sb + hb : nullptr, p.s0_sr, p.s0_sc, 0.0f);
-                    // the earlier segments' own states, in the order of work
-                    if (kMode == kStates)
+                    // the initial state, and (kStates) the earlier segments' own in the order of work,
+                    // each with what came before it decayed
 #pragma unroll 1
-                        for (int j = 0; j < it.j; ++j) {
-                            const int s = rev ? it.ng - 1 - j : j, n = it.len - s * a.seg < a.seg ? it.len - s * a.seg : a.seg;
-                            add(p.seg_states + (int64_t)(it.slot0 + s) * sb + hb, p.seg_sr, p.seg_sc, expf((float)n * g));
+                    for (int j = -1; j < (kMode == kStates ? it.j : 0); ++j) {
+                        const float *from = p.s0 ? p.s0 + it.seq * sb + hb : nullptr;
+                        int64_t sr = p.s0_sr, sc = p.s0_sc;
+                        float decay = 0.0f;
+                        if (kMode == kStates && j >= 0) {
+                            const int i = rev ? it.ng - 1 - j : j, n = it.len - i * a.seg < a.seg ? it.len - i * a.seg : a.seg;
+                            from = p.seg_states + (int64_t)(it.slot0 + i) * sb + hb;
+                            sr = p.seg_sr;
+                            sc = p.seg_sc;
+                            decay = expf((float)n * g);
                         }
+                        if (from == nullptr) continue;
+                        if (kMode == kStates && sc == 1) {
+                            // (few items: the way through shared memory below costs registers in the chunks' loop)
+#pragma unroll
+                            for (int i = 0; i < NCOL; i += 4) {
+                                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                                if (row < p.dx && col0 + i < p.dz) u = *reinterpret_cast<const uint4 *>(from + row * sr + col0 + i);
+                                S[i / 2] = f2_fma(f2_splat(decay), S[i / 2], f2_make(__uint_as_float(u.x), __uint_as_float(u.y)));
+                                S[i / 2 + 1] = f2_fma(f2_splat(decay), S[i / 2 + 1], f2_make(__uint_as_float(u.z), __uint_as_float(u.w)));
+                            }
+                        } else if (sc == 1) {  // (and 16-byte aligned: dz is a multiple of 8)
+#pragma unroll
+                            for (int h0 = 0; h0 < NCOL; h0 += kPc) {
+                                uint4 v[32 / kPr];
+#pragma unroll
+                                for (int i = 0; i < 32 / kPr; ++i) {
+                                    const int r = pr + kPr * i;
+                                    v[i] = make_uint4(0u, 0u, 0u, 0u);
+                                    if (row0 + r < p.dx && col0 + h0 + 4 * pq < p.dz)
+                                        v[i] = *reinterpret_cast<const uint4 *>(from + (row0 + r) * sr + col0 + h0 + 4 * pq);
+                                }
+                                __syncwarp();
+#pragma unroll
+                                for (int i = 0; i < 32 / kPr; ++i) sts128(piece(pr + kPr * i, pq), v[i].x, v[i].y, v[i].z, v[i].w);
+                                __syncwarp();
+#pragma unroll
+                                for (int i = 0; i < kPc; i += 4) {
+                                    const uint4 u = lds128(piece(lane, i / 4));
+                                    f2 &a0 = S[(h0 + i) / 2], &a1 = S[(h0 + i) / 2 + 1];
+                                    a0 = f2_fma(f2_splat(decay), a0, f2_make(__uint_as_float(u.x), __uint_as_float(u.y)));
+                                    a1 = f2_fma(f2_splat(decay), a1, f2_make(__uint_as_float(u.z), __uint_as_float(u.w)));
+                                }
+                            }
+                        } else {
+                            const int64_t at = row * sr + col0 * sc;  // (rows are neighbours)
+#pragma unroll
+                            for (int i = 0; i < NCOL; i += 2) {
+                                const bool use = row < p.dx && col0 + i < p.dz;
+                                const float u = use ? from[at + i * sc] : 0.0f, v = use ? from[at + (i + 1) * sc] : 0.0f;
+                                S[i / 2] = f2_fma(f2_splat(decay), S[i / 2], f2_make(u, v));
+                            }
+                        }
+                    }
                 }
             }
             // lam^n S as keep S + part S, rounded once: with lam^n >= 1/2 part = lam^n - 1 keeps the
@@ -969,18 +1010,36 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
                 if (lane == 0) bar_arrive(bar(kBarKVFree));
             }
             if (kMode == kChained && !kOwn && !it.last) {
-                float4 *to = reinterpret_cast<float4 *>(a.chain + ((int64_t)chain * DX + row) * kZ + c0);
+                float4 *to = reinterpret_cast<float4 *>(a.chain) + ((int64_t)chain * (kZ / 4) + c0 / 4) * DX + row;
 #pragma unroll
-                for (int i = 0; i < NCOL; i += 4) *reinterpret_cast<ulonglong2 *>(to + i / 4) = make_ulonglong2(S[i / 2], S[i / 2 + 1]);
+                for (int i = 0; i < NCOL; i += 4)
+                    *reinterpret_cast<ulonglong2 *>(to + (i / 4) * DX) = make_ulonglong2(S[i / 2], S[i / 2 + 1]);
                 __threadfence();
                 __syncwarp();
                 if (lane == 0) atomicAdd(a.flags + chain, 1);
-            } else if (p.fin && (kOwn || it.last) && row < p.dx) {
+            } else if (p.fin && (kOwn || it.last)) {
                 const int64_t to = kOwn ? it.slot0 + (rev ? it.ng - 1 - it.j : it.j) : it.seq;
-                float *f = p.fin + to * sb + hb + row * (int64_t)p.dz + col0;
+                float *f = p.fin + to * sb + hb + col0 + 4 * pq;
+                if (DX == 128 && !kOwn && cc > 0 && !wait_all(kBarOB, cc - 1)) return false;
 #pragma unroll
-                for (int i = 0; i < NCOL; i += 4)
-                    if (col0 + i < p.dz) *reinterpret_cast<ulonglong2 *>(f + i) = make_ulonglong2(S[i / 2], S[i / 2 + 1]);
+                for (int h0 = 0; h0 < NCOL; h0 += kPc) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < kPc; i += 4) {
+                        float x, y, z, u;
+                        f2_split(S[(h0 + i) / 2], x, y);
+                        f2_split(S[(h0 + i) / 2 + 1], z, u);
+                        sts128(piece(lane, i / 4), __float_as_uint(x), __float_as_uint(y), __float_as_uint(z), __float_as_uint(u));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 32 / kPr; ++i) {
+                        const int r = pr + kPr * i;
+                        if (row0 + r < p.dx && col0 + h0 + 4 * pq < p.dz)
+                            *reinterpret_cast<uint4 *>(f + (row0 + r) * (int64_t)p.dz + h0) = lds128(piece(r, pq));
+                    }
+                }
+                __syncwarp();
             }
             return true;
         });
