@@ -32,6 +32,13 @@
 // KV takes the three parts of Z' as one product of N = 192 (24 products of N = 64
 // read Y three times, and took 1900 clocks a chunk against 1200).
 //
+// Measured at one chain per SM (148 heads, 4096 tokens): a chunk takes 2.0 us at dk =
+// dv = 64 (64 KB from and to HBM: 4.7 TB/s), 2.8 us at dk = 128, dv = 64 (96 KB, 5.1
+// TB/s); 8 x 2048 tokens x 24 heads of 64 take 64 us. What bounds it is the roles'
+// instructions, some 7000 a chunk, half of the issue slots, and the instruction cache
+// they share: loops unrolled twice as far took 10 to 25 % more, a third and fourth stage
+// with a ring of its own for Z nothing less.
+//
 // Three ways to cut the work, by the number of (sequence, head, column block)s, each
 // of which is a chain of chunks (see plan_of):
 //   kWhole    an item is a whole sequence;
@@ -357,7 +364,8 @@ __device__ __forceinline__ int segments_of(const TcArgs &a, int i, int &row0, in
 // gets the same answer in every lane.
 template <bool kOwn>
 struct Finder {
-    int j = 0, before = 0;  // packed: the level, and the (sequence, segment)s before it
+    // packed: the level, a block of 32 sequences, and the (sequence, segment)s before it and before the level
+    int j = 0, i0 = 0, before = 0, level0 = 0;
     __device__ __forceinline__ bool find(const TcArgs &a, int n, int lane, Item &it) {
         it.unit = n % a.units;
         n /= a.units;
@@ -369,20 +377,22 @@ struct Finder {
             j = n / a.batch;
             if (j >= a.nseg - (kOwn ? 1 : 0)) return false;
         } else {
-            for (;; ++j) {
-                int k = n - before, count = 0;
-                it.seq = -1;
-                for (int i0 = 0; i0 < a.batch; i0 += 32) {
-                    const int i = i0 + lane;
-                    const unsigned m =
-                        __ballot_sync(0xffffffffu, i < a.batch && segments_of(a, i, row0, len, slot0) - (kOwn ? 1 : 0) > j);
-                    if (it.seq < 0 && k < __popc(m)) it.seq = i0 + (int)__fns(m, 0, k + 1);
-                    k -= __popc(m);
-                    count += __popc(m);
+            for (;;) {
+                const int i = i0 + lane;
+                const unsigned m =
+                    __ballot_sync(0xffffffffu, i < a.batch && segments_of(a, i, row0, len, slot0) - (kOwn ? 1 : 0) > j);
+                if (n - before < __popc(m)) {
+                    it.seq = i0 + (int)__fns(m, 0, n - before + 1);
+                    break;
                 }
-                if (it.seq >= 0) break;
-                if (count == 0) return false;
-                before += count;
+                before += __popc(m);
+                i0 += 32;
+                if (i0 >= a.batch) {
+                    if (before == level0) return false;  // no sequence has so many segments
+                    level0 = before;
+                    i0 = 0;
+                    ++j;
+                }
             }
         }
         ng = segments_of(a, it.seq, row0, len, slot0);
@@ -716,7 +726,7 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
             const int t0 = 32 * (warp - R::kE0), t = t0 + lane;
             const uint32_t lanes = tmem + ((uint32_t)t0 << 16);
             // A thread holds a row, but stores that touch 32 rows at once keep the load-store unit
-            // from everybody else (2000 clocks a chunk): rows go through the chunk's Z tile, which
+            // from everybody else (2000 clocks a chunk, a quarter of the whole): rows go through the chunk's Z tile, which
             // nothing reads any more, and leave 128 bytes of 4 rows at a time.
             const int q = lane & 7, r4 = lane >> 3;
             const uint32_t zrow = (uint32_t)(M::kX + M::kY) + 128u * t;

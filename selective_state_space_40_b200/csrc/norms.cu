@@ -112,7 +112,7 @@ __device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
 
 // Rows on their way through shared memory: NA arrays' rows a stage, brought by bulk
 // copies, so that several rows of a block are in flight without holding registers
-// (the gated backward of 5120 bf16 columns: NNN us, NNN with one row in registers).
+// (the gated backward of 8192 x 5120 in bf16: 102 us, 109 us with rows straight to registers).
 // For blocks of one group; row k of a block is in stage k % stages, phase k / stages.
 template <int NA>
 struct Ring {

@@ -166,6 +166,67 @@ def test_segments_of_packed_sequences():
     run_packed(make(4300, 2, 2, 128, 64, BF, 31, n=5, decays=[-2.0 ** -11, -0.02]), starts, BF)
 
 
+@pytest.mark.parametrize("b,L,H,G,dk,dv", [(8, 700, 24, 24, 16, 16), (5, 530, 33, 11, 128, 8)])
+def test_chains_that_do_not_divide_by_the_sms(b, L, H, G, dk, dv):
+    """Sequences in several items, the state handed from one CTA to the next."""
+    run_dense(make(b * L, H, G, dk, dv, BF, L, n=b), b, L, BF)
+
+
+def test_many_short_packed_sequences():
+    r = np.random.RandomState(3)
+    lens = r.randint(0, 40, 150).tolist() + [300] + [0] * 40 + [7]
+    starts = np.cumsum([0] + lens).tolist()
+    run_packed(make(starts[-1] + 3, 4, 4, 16, 24, BF, 33, n=len(lens)), starts, BF)
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Arrays of more than 2^32 elements: with nothing remembered, o_t = a (q_t . k_t) v_t, whole and at both ends."""
+    L, H, d = 270000, 128, 128
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    q = torch.empty(1, L, H, d, dtype=BF, device=DEV)
+    assert q.numel() > 2 ** 32
+    q.normal_(generator=gen)
+    o, fin = mb.linattn_fwd(q, q, q, torch.full((H,), float("-inf"), device=DEV), scale=1.0)
+    for sl in (slice(0, 300), slice(L - 300, L)):
+        x = q[0, sl].double()
+        want = x.square().sum(-1, keepdim=True) * x
+        assert ((o[0, sl].double() - want).norm() / want.norm()).item() <= 4e-3
+    x = q[0, -1].double()
+    assert ((fin[0].double() - x[:, :, None] * x[:, None, :]).norm() / fin.double().norm()).item() <= 1e-6
+    # and gradients through rows of a wide buffer, 2^32 elements behind its start
+    wide = q.view(-1)
+    n, tail = 200, q.view(-1).numel() - 200 * H * d
+    t = wide[tail:].view(1, n, H, d)
+    gr = mb.linattn_bwd(t, t, t, torch.full((H,), -0.5, device=DEV), t, scale=1.0)
+    c = t.clone()
+    ref = mb.linattn_bwd(c, c, c, torch.full((H,), -0.5, device=DEV), c, scale=1.0)
+    assert all(torch.equal(gr[m], ref[m]) for m in ("dq", "dk", "dv", "dinitial_state"))
+
+
+def test_two_streams_with_their_own_workspaces():
+    """Two long calls at once, each with its own workspace: the results of one after the other."""
+    xs = [make(4096, 2, 2, 64, 64, BF, 80 + i, n=1, decays=[-0.001, -0.02]) for i in range(2)]
+    ins = [dev(x, "q", "k", "v", "g") for x in xs]
+    want = [mb.linattn_fwd(q[None], k[None], v[None], g) for q, k, v, g in ins]
+    need = mb.mamba_linattn_workspace_size(mb.linattn_dims_for(*(t[None] for t in ins[0][:3]), ins[0][0][None]), False)
+    assert need > 0
+    ws = [torch.empty(need, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for (q, k, v, g), w, st in zip(ins, ws, streams):
+            with torch.cuda.stream(st):
+                got.append(mb.linattn_fwd(q[None], k[None], v[None], g, workspace=w))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+    with pytest.raises(mb.MambaScanError) as e:
+        mb.linattn_fwd(*(t[None] for t in ins[0][:3]), ins[0][3], workspace=ws[0][:need - 1])
+    assert e.value.code == mb.MS_ERR_WORKSPACE
+    with pytest.raises(ValueError, match="tensors on"):
+        mb.linattn_fwd(*(t[None] for t in ins[0][:3]), ins[0][3].cpu())
+
+
 def test_decay_extremes():
     """exp(log_decay) = 0 (the token alone), subnormal steps of the powers, and no decay at all."""
     x = make(300, 5, 5, 64, 64, BF, 41, n=1, decays=[float("-inf"), -80.0, -5.0, 0.0, -2.0 ** -20])
@@ -322,3 +383,45 @@ def test_step_strides_and_repeat():
     outs = [mb.linattn_state_update(st, q[:, t], k[:, t], v[:, t], g) for t in range(T)]
     check_fwd(x, [0, T, 2 * T], torch.stack(outs, 1).flatten(0, 1), st, F32)
     assert (pool[:, 0] == 9.0).all() and (pool[:, -1] == 9.0).all()
+
+
+def test_prompt_then_tokens_in_a_graph():
+    """Forward over a prompt, then captured steps from its state: the forward over all tokens."""
+    b, L, T, H, G, d = 2, 150, 6, 4, 2, 64
+    x = make(b * (L + T), H, G, d, d, BF, 90, n=b)
+    q, k, v = (x[n].view(b, L + T, -1, d).to(DEV) for n in ("q", "k", "v"))
+    g = x["g"].to(DEV)
+    o, st = mb.linattn_fwd(q[:, :L], k[:, :L], v[:, :L], g, initial_state=x["s0"].to(DEV))
+    first = st.clone()
+    tok = [t[:, L].clone() for t in (q, k, v)]
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        mb.linattn_state_update(st, *tok, g)  # (loads the kernel before the capture)
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        y = mb.linattn_state_update(st, *tok, g)
+    st.copy_(first)
+    outs = [o]
+    for t in range(T):
+        for a, full in zip(tok, (q, k, v)):
+            a.copy_(full[:, L + t])
+        graph.replay()
+        outs.append(y[:, None].clone())
+    check_fwd(x, [0, L + T, 2 * (L + T)], torch.cat(outs, 1).flatten(0, 1), st, BF)
+
+
+def test_step_state_beyond_32_bit_offsets():
+    """Two rows' states 2^32 elements apart in one pool."""
+    H, dk, dv = 2, 64, 64
+    pool = torch.zeros(2 ** 32 + H * dk * dv, device=DEV)
+    st = pool.as_strided((2, H, dk, dv), (2 ** 32, dk * dv, dv, 1))
+    x = make(2, H, H, dk, dv, F32, 5, n=2)
+    st.copy_(x["s0"])
+    q, k, v, g = dev(x, "q", "k", "v", "g")
+    o = mb.linattn_state_update(st, q, k, v, g, x["scale"])
+    dense = x["s0"].to(DEV)
+    ref = mb.linattn_state_update(dense, q, k, v, g, x["scale"])
+    assert torch.equal(o, ref) and torch.equal(st, dense)
+    assert pool[H * dk * dv:H * dk * dv + 1000].abs().max() == 0
