@@ -418,6 +418,9 @@ int mamba2_ssd_state_update(float *state, const void *x, const void *dt, const f
  * out and MS_ERR_SHAPE is ORed into dev_status; where the offsets decrease,
  * the other sequences' results are undefined too (nothing outside the arrays
  * is touched).
+ * Arrays that are read may be broadcast (stride 0); one that is written holds
+ * no element twice (MS_ERR_STRIDE), and overlaps no other array of its call
+ * except where that is said.
  * dk and dv are 1..128, all arrays of one type, bf16 or fp32. bf16 rows that
  * start on 16-byte boundaries (every pointer and stride) with dk and dv
  * multiples of 8 run on the tcgen05 tensor cores in chunks of 128 tokens:
@@ -465,8 +468,10 @@ int mamba_linattn_fwd(const void *q, const void *k, const void *v, const float *
  *     dinitial_state = lam R_0
  * dk and dv of a shared kv head are sums over its heads, in a fixed order.
  * dq, dk, dv have the layouts and strides of q, k, v; dinitial_state (fp32,
- * dense; NULL = not wanted) must not be dfinal (MS_ERR_SHAPE). Each result is
- * rounded once to its type. workspace: as for the forward, of
+ * dense; NULL = not wanted) must be neither dfinal nor initial_state
+ * (MS_ERR_SHAPE). q, k and v must not be broadcast here: their gradients would
+ * be (MS_ERR_STRIDE; kv_heads says which heads share). dout may be. Each result
+ * is rounded once to its type. workspace: as for the forward, of
  * mamba_linattn_bwd_workspace_size() bytes.
  */
 size_t mamba_linattn_bwd_workspace_size(const ms_linattn_dims *dims, int packed);
@@ -503,7 +508,8 @@ int mamba_linattn_state_update(float *state, const void *q, const void *k, const
  *     y = n(x silu(z)) w          (gate_first nonzero, as the Mamba-2 block)
  * x, z, y [rows, width] in one type with their own row strides; weight [width]
  * fp32 (NULL = 1); z NULL = no gate. Statistics are fp32. A group is at most
- * 16384 columns wide (MS_ERR_SHAPE).
+ * 16384 columns wide (MS_ERR_SHAPE). Inputs' rows may be broadcast (stride 0),
+ * written ones not (MS_ERR_STRIDE); outputs overlap no input.
  */
 typedef struct {
     int64_t rows, width, groups;
@@ -533,7 +539,7 @@ int mamba_gated_norm_bwd(const void *x, const void *z, const float *weight, cons
  * the optional scale per channel,
  *     residual_out = residual + s c x       y = n(residual_out) w
  * x, y [rows, width] in dtype; residual (NULL = 0), residual_out (NULL = not
- * wanted; may be residual itself) in res_dtype; weight, channel_scale [width]
+ * wanted; may be residual itself, with its stride) in res_dtype; weight, channel_scale [width]
  * fp32 (NULL = 1). y is formed from the sum before its rounding to res_dtype.
  * width is at most 16384.
  */

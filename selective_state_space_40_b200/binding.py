@@ -697,8 +697,10 @@ def state_update(state, x, delta, A, B, C, D=None, z=None, delta_bias=None, soft
 _cuda = None  # torch's own entry points for the current device and stream, looked up once
 
 
-def _layer_call(ref, stream, *others):
-    """The stream handle for a call on ``ref``'s device, every tensor checked
+# The conveniences below run under ``stream`` where one is given, what they allocate too:
+# results and workspaces then belong to the stream that uses them.
+def _layer_call(ref, *others):
+    """The current stream's handle for a call on ``ref``'s device, every tensor checked
     to be on that device and the device to be the current one (the library
     launches on the current device)."""
     global _cuda
@@ -715,7 +717,7 @@ def _layer_call(ref, stream, *others):
                  raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
     if dev != _cuda[0]():
         raise ValueError(f"tensors on {ref.device}, but cuda:{_cuda[0]()} is the current device")
-    return _cuda[1](dev) if stream is None else stream.cuda_stream
+    return _cuda[1](dev)
 
 
 def _same_type(t, shape, dtype, name):
@@ -780,6 +782,10 @@ def linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, seq_start=Non
     ``final_state`` may be ``initial_state``. ``workspace`` (uint8 CUDA tensor
     of at least ``mamba_linattn_workspace_size`` bytes) is allocated per call
     when omitted. Returns (o, final_state or None)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return linattn_fwd(q, k, v, log_decay, scale, seq_start, initial_state, o, final_state,
+                               return_final_state, None, dev_status, workspace)
     n, H, dk, dv, oshape = _check_linattn(q, k, v, log_decay, seq_start)
     if o is None:
         o = q.new_empty(oshape)
@@ -790,7 +796,7 @@ def linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, seq_start=Non
         fs = log_decay.new_empty((n, H, dk, dv))
     _dense_f32(initial_state, (n, H, dk, dv), "initial_state")
     _dense_f32(final_state, (n, H, dk, dv), "final_state")
-    st = _layer_call(q, stream, k, v, log_decay, seq_start, initial_state, o, fs, dev_status, workspace)
+    st = _layer_call(q, k, v, log_decay, seq_start, initial_state, o, fs, dev_status, workspace)
     dims = linattn_dims_for(q, k, v, o, seq_start)
     ws, wp, wb = _workspace(workspace, mamba_linattn_workspace_size(dims, seq_start is not None), q.device)
     rc = mamba_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), dk ** -0.5 if scale is None else scale,
@@ -805,7 +811,12 @@ def linattn_bwd(q, k, v, log_decay, dout, scale: Optional[float] = None, seq_sta
     """Gradients of linattn_fwd for dL/do = dout and dL/dfinal_state = dfinal:
     a dict dq, dk, dv (types and layouts of q, k, v) and dinitial_state (fp32,
     None unless wanted). ``grads`` may hold preallocated dq, dk, dv with the
-    strides of q, k, v (rows of no sequence keep what they held)."""
+    strides of q, k, v (rows of no sequence keep what they held). q, k and v
+    must not be broadcast: their gradients would be."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return linattn_bwd(q, k, v, log_decay, dout, scale, seq_start, initial_state, dfinal, want_dinitial,
+                               grads, None, dev_status, workspace)
     torch = _torch()
     n, H, dk, dv, oshape = _check_linattn(q, k, v, log_decay, seq_start)
     _same_type(dout, oshape, q.dtype, "dout")
@@ -820,7 +831,7 @@ def linattn_bwd(q, k, v, log_decay, dout, scale: Optional[float] = None, seq_sta
             raise ValueError(f"{name} must have the shape, type and strides of {name[1]}")
         g[name] = got
     g["dinitial_state"] = torch.empty((n, H, dk, dv), dtype=torch.float32, device=q.device) if want_dinitial else None
-    st = _layer_call(q, stream, k, v, log_decay, seq_start, initial_state, dout, dfinal, g["dq"], g["dk"], g["dv"],
+    st = _layer_call(q, k, v, log_decay, seq_start, initial_state, dout, dfinal, g["dq"], g["dk"], g["dv"],
                      dev_status, workspace)
     dims = linattn_dims_for(q, k, v, dout, seq_start)
     ws, wp, wb = _workspace(workspace, mamba_linattn_bwd_workspace_size(dims, seq_start is not None), q.device)
@@ -837,6 +848,9 @@ def linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] = Non
     """One token of linattn_fwd: state [b, H, dk, dv] fp32 (dense [dk, dv]
     blocks, updated in place), q [b, H, dk], k [b, G, dk], v [b, G, dv].
     Returns o [b, H, dv]."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return linattn_state_update(state, q, k, v, log_decay, scale, o, None, dev_status)
     b, H, dk = q.shape
     G, dv = v.shape[1], v.shape[2]
     ss = state.stride()
@@ -850,7 +864,7 @@ def linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] = Non
         o = q.new_empty((b, H, dv))
     else:
         _same_type(o, (b, H, dv), q.dtype, "o")
-    st = _layer_call(state, stream, q, k, v, log_decay, o, dev_status)
+    st = _layer_call(state, q, k, v, log_decay, o, dev_status)
     qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
     dims = LinattnUpdateDims(b, H, G, dk, dv, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], ss[0], ss[1],
                              _dtype_code(q))
@@ -876,12 +890,15 @@ def gated_norm_fwd(x, z=None, weight=None, groups: int = 1, eps: float = 1e-5, g
     """Gated group norm (see include/mambascan.h, mamba_gated_norm_fwd) of x
     [rows, width]: norm(x) w silu(z), or norm(x silu(z)) w with
     ``gate_first``. Returns y."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return gated_norm_fwd(x, z, weight, groups, eps, gate_first, y, None, dev_status)
     xs = _rows(x, "x", x.shape, x.dtype)
     zs = _rows(z, "z", x.shape, x.dtype)
     _dense_f32(weight, x.shape[1:], "weight")
     if y is None:
         y = x.new_empty(x.shape)
-    st = _layer_call(x, stream, z, weight, y, dev_status)
+    st = _layer_call(x, z, weight, y, dev_status)
     dims = GatedNormDims(x.shape[0], x.shape[1], groups, xs, zs, _rows(y, "y", x.shape, x.dtype), eps, _dtype_code(x),
                          int(gate_first))
     rc = mamba_gated_norm_fwd(_ptr(x), _ptr(z), _ptr(weight), _ptr(y), dims, _ptr(dev_status), st)
@@ -894,6 +911,9 @@ def gated_norm_bwd(x, z, weight, dy, groups: int = 1, eps: float = 1e-5, gate_fi
                    want_dweight: bool = True, stream=None, dev_status=None, workspace=None):
     """Gradients of gated_norm_fwd: a dict dx, dz (None without z), dweight
     (fp32; None unless wanted)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return gated_norm_bwd(x, z, weight, dy, groups, eps, gate_first, want_dweight, None, dev_status, workspace)
     torch = _torch()
     xs = _rows(x, "x", x.shape, x.dtype)
     zs = _rows(z, "z", x.shape, x.dtype)
@@ -901,7 +921,7 @@ def gated_norm_bwd(x, z, weight, dy, groups: int = 1, eps: float = 1e-5, gate_fi
     g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
          "dz": torch.empty(x.shape, dtype=x.dtype, device=x.device) if z is not None else None,
          "dweight": torch.empty(x.shape[1], dtype=torch.float32, device=x.device) if want_dweight else None}
-    st = _layer_call(x, stream, z, weight, dy, dev_status, workspace)
+    st = _layer_call(x, z, weight, dy, dev_status, workspace)
     dims = GatedNormDims(x.shape[0], x.shape[1], groups, xs, zs, _rows(dy, "dy", x.shape, x.dtype), eps,
                          _dtype_code(x), int(gate_first))
     ws, wp, wb = _workspace(workspace, mamba_gated_norm_bwd_workspace_size(dims) if want_dweight else 0, x.device)
@@ -919,6 +939,10 @@ def residual_norm_fwd(x, residual=None, weight=None, eps: float = 1e-5, res_scal
     channel_scale x, y = norm(residual_out) weight. ``residual_out`` (of the
     residual's type, else of ``residual_dtype``, else x's) may be
     ``residual``. Returns (y, residual_out)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return residual_norm_fwd(x, residual, weight, eps, res_scale, channel_scale, y, residual_out,
+                                     residual_dtype, None, dev_status)
     shape = x.shape
     xs = _rows(x, "x", shape, x.dtype)
     rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else \
@@ -929,7 +953,7 @@ def residual_norm_fwd(x, residual=None, weight=None, eps: float = 1e-5, res_scal
         y = x.new_empty(shape)
     _dense_f32(weight, shape[1:], "weight")
     _dense_f32(channel_scale, shape[1:], "channel_scale")
-    st = _layer_call(x, stream, residual, weight, channel_scale, y, residual_out, dev_status)
+    st = _layer_call(x, residual, weight, channel_scale, y, residual_out, dev_status)
     dims = ResidualNormDims(shape[0], shape[1], xs, _rows(residual, "residual", shape, rt),
                             _rows(y, "y", shape, x.dtype), _rows(residual_out, "residual_out", shape, rt), eps,
                             res_scale, _dtype_code(x), _dtype_code(residual_out))
@@ -945,6 +969,10 @@ def residual_norm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, eps:
     """Gradients of residual_norm_fwd from its sum ``residual_out``: a dict dx
     (dy's type), dresidual (the sum's type), dweight and, where x and
     channel_scale are given, dchannel_scale (fp32)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return residual_norm_bwd(residual_out, weight, dy, dresidual_out, x, eps, res_scale, channel_scale,
+                                     want_dweight, None, dev_status, workspace)
     torch = _torch()
     shape = dy.shape
     rs = _rows(residual_out, "residual_out", shape, residual_out.dtype)
@@ -956,7 +984,7 @@ def residual_norm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, eps:
          "dresidual": torch.empty(shape, dtype=residual_out.dtype, device=dy.device),
          "dweight": torch.empty(shape[1], **f32) if want_dweight else None,
          "dchannel_scale": torch.empty(shape[1], **f32) if with_c else None}
-    st = _layer_call(dy, stream, residual_out, weight, dresidual_out, x, channel_scale, dev_status, workspace)
+    st = _layer_call(dy, residual_out, weight, dresidual_out, x, channel_scale, dev_status, workspace)
     dims = ResidualNormDims(shape[0], shape[1], _rows(x, "x", shape, dy.dtype),
                             _rows(dresidual_out, "dresidual_out", shape, residual_out.dtype),
                             _rows(dy, "dy", shape, dy.dtype), rs, eps, res_scale, _dtype_code(dy),

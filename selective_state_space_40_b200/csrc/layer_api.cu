@@ -2,6 +2,7 @@
 // of the norms around it: host-side argument checks, workspaces and launches.
 // The operations are described in include/mambascan.h.
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -23,6 +24,22 @@ bool offsets_ok(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int6
     return o <= (__int128)INT64_MAX / 8;
 }
 
+// Whether an array of these extents and strides, rows of n3 dense elements at the
+// end, holds no element twice: each dimension steps over all that the smaller steps span.
+bool distinct(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int64_t n3) {
+    struct Dim {
+        int64_t s, n;
+    } d[3] = {{s0, n0}, {s1, n1}, {s2, n2}};
+    std::sort(d, d + 3, [](const Dim &x, const Dim &y) { return x.s < y.s; });
+    __int128 span = n3;
+    for (const Dim &x : d) {
+        if (x.n <= 1) continue;
+        if (x.s < span) return false;
+        span += (__int128)(x.n - 1) * x.s;
+    }
+    return true;
+}
+
 int num_sms_current() {
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -38,8 +55,9 @@ int cuda_rc(cudaError_t e) {
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Sizes, strides and types of a linear-attention call, with its token arrays
-// as pointers (q, k, v, o or dout, and the gradients).
-int check_linattn(const ms_linattn_dims *d, bool packed, const void *const *tok, int ntok, const float *const *f32,
+// as pointers (q, k, v, o or dout, and the gradients). Arrays that are written
+// must not hold an element twice: o, or (bwd) what has the strides of q, k and v.
+int check_linattn(const ms_linattn_dims *d, bool packed, bool bwd, const void *const *tok, int ntok, const float *const *f32,
                   int nf32, const int32_t *seq_start) {
     if (!d) return MS_ERR_NULL;
     if (!dtype_ok(d->dtype)) return MS_ERR_DTYPE;
@@ -57,11 +75,19 @@ int check_linattn(const ms_linattn_dims *d, bool packed, const void *const *tok,
             !offsets_ok(nb, d->k_sb, rows, d->k_sl, G, d->k_sh, d->dk) ||
             !offsets_ok(nb, d->v_sb, rows, d->v_sl, G, d->v_sh, d->dv) ||
             !offsets_ok(nb, d->o_sb, rows, d->o_sl, H, d->o_sh, d->dv) ||
-            !offsets_ok(nb, rows * H, rows, H, 1, 0, 1) ||
+            (__int128)nb * rows * H * 128 > (__int128)INT64_MAX / 8 ||
             (__int128)d->batch * d->nheads * d->dk * d->dv > (__int128)INT64_MAX / 8)
             return MS_ERR_SHAPE;
     }
     if ((__int128)d->batch * d->nheads > INT32_MAX) return MS_ERR_SHAPE;
+    if (rows > 0) {
+        const int64_t H = d->nheads, G = d->kv_heads;
+        if (!bwd && !distinct(nb, d->o_sb, rows, d->o_sl, H, d->o_sh, d->dv)) return MS_ERR_STRIDE;
+        if (bwd && (!distinct(nb, d->q_sb, rows, d->q_sl, H, d->q_sh, d->dk) ||
+                    !distinct(nb, d->k_sb, rows, d->k_sl, G, d->k_sh, d->dk) ||
+                    !distinct(nb, d->v_sb, rows, d->v_sl, G, d->v_sh, d->dv)))
+            return MS_ERR_STRIDE;
+    }
     if (d->batch == 0) return MS_OK;
     if (!f32[0]) return MS_ERR_NULL;  // log_decay
     if (rows > 0)
@@ -151,12 +177,13 @@ int mamba_linattn_fwd(const void *q, const void *k, const void *v, const float *
     const void *tok[] = {q, k, v, o};
     const float *f32[] = {log_decay, initial_state, final_state};
     const bool packed = seq_start != nullptr;
-    int rc = check_linattn(d, packed, tok, 4, f32, 3, seq_start);
+    int rc = check_linattn(d, packed, false, tok, 4, f32, 3, seq_start);
     if (rc != MS_OK) return rc;
     if (d->batch == 0) return MS_OK;
     const size_t need = mamba_linattn_workspace_size(d, packed);
     if (workspace_bytes < need || (need > 0 && !workspace)) return MS_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 16)) return MS_ERR_ALIGN;
+    if (o && (o == q || o == k || o == v)) return MS_ERR_SHAPE;
     const int share = (int)(d->nheads / d->kv_heads), dk = (int)d->dk, dv = (int)d->dv;
     ms::LaArgs a = la_args(d, log_decay, seq_start, dev_status);
     a.np = 1;
@@ -178,13 +205,17 @@ int mamba_linattn_bwd(const void *q, const void *k, const void *v, const float *
     const void *tok[] = {q, k, v, dout, dq, dk_, dv_};
     const float *f32[] = {log_decay, initial_state, dfinal, dinitial_state};
     const bool packed = seq_start != nullptr;
-    int rc = check_linattn(d, packed, tok, 7, f32, 4, seq_start);
+    int rc = check_linattn(d, packed, true, tok, 7, f32, 4, seq_start);
     if (rc != MS_OK) return rc;
     if (d->batch == 0) return MS_OK;
-    if (dinitial_state && dinitial_state == dfinal) return MS_ERR_SHAPE;
+    if (dinitial_state && (dinitial_state == dfinal || dinitial_state == initial_state)) return MS_ERR_SHAPE;
     const size_t need = mamba_linattn_bwd_workspace_size(d, packed);
     if (workspace_bytes < need || (need > 0 && !workspace)) return MS_ERR_WORKSPACE;
     if (need > 0 && !aligned(workspace, 16)) return MS_ERR_ALIGN;
+    for (const void *g : {dq, dk_, dv_})
+        for (const void *in : {q, k, v, dout})
+            if (g && g == in) return MS_ERR_SHAPE;
+    if (dq && (dq == dk_ || dq == dv_ || dk_ == dv_)) return MS_ERR_SHAPE;
     const int share = (int)(d->nheads / d->kv_heads), dk = (int)d->dk, dv = (int)d->dv;
     const bool bf16 = d->dtype == MS_BF16;
     const cudaStream_t st = (cudaStream_t)stream;
@@ -209,6 +240,7 @@ int mamba_linattn_bwd(const void *q, const void *k, const void *v, const float *
     if (e == cudaSuccess && share > 1) {
         ms::LaReduceArgs r{};
         r.seq_start = seq_start;
+        r.status = dev_status;
         r.batch = d->batch; r.seqlen = d->seqlen; r.total = d->total; r.H = d->nheads; r.kv = d->kv_heads;
         r.part = reinterpret_cast<const float *>(ws);
         r.out = dk_; r.d = dk; r.o_sb = d->k_sb; r.o_sl = d->k_sl; r.o_sh = d->k_sh;
@@ -243,7 +275,9 @@ int mamba_linattn_state_update(float *state, const void *q, const void *k, const
         !offsets_ok(d->batch, d->v_sb, G, d->v_sh, 1, 0, d->dv) || !offsets_ok(d->batch, d->o_sb, H, d->o_sh, 1, 0, d->dv))
         return MS_ERR_SHAPE;
     // two heads' (or rows') states in the same memory would be updated twice, in no order
-    if ((H > 1 && d->state_sh < d->dk * d->dv) || (d->batch > 1 && d->state_sb < d->dk * d->dv)) return MS_ERR_STRIDE;
+    if (!distinct(d->batch, d->state_sb, H, d->state_sh, 1, 0, d->dk * d->dv) ||
+        !distinct(d->batch, d->o_sb, H, d->o_sh, 1, 0, d->dv))
+        return MS_ERR_STRIDE;
     ms::LaUpdateArgs a{};
     a.state = state; a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.o = o; a.status = dev_status;
     a.batch = d->batch; a.H = H; a.kv = G; a.dk = (int)d->dk; a.dv = (int)d->dv;
@@ -288,6 +322,7 @@ int mamba_gated_norm_fwd(const void *x, const void *z, const float *weight, void
     if (!x || !y) return MS_ERR_NULL;
     const int es = elem_bytes(d->dtype);
     if (!aligned(x, es) || !aligned(z, es) || !aligned(y, es) || !aligned(weight, 4)) return MS_ERR_ALIGN;
+    if (!distinct(d->rows, d->y_sr, 1, 0, 1, 0, d->width)) return MS_ERR_STRIDE;
     ms::GatedNormArgs a = gated_args(d, x, z, weight, dev_status);
     a.y = y;
     return cuda_rc(ms::launch_gated_norm(a, d->dtype == MS_BF16, false, num_sms_current(), (cudaStream_t)stream));
@@ -354,6 +389,11 @@ int mamba_residual_norm_fwd(const void *x, const void *residual, const float *we
     if (!aligned(x, es) || !aligned(y, es) || !aligned(residual, rs) || !aligned(residual_out, rs) ||
         !aligned(weight, 4) || !aligned(channel_scale, 4))
         return MS_ERR_ALIGN;
+    // rows written twice; or, in place, one row's sum over another row that is still to be read
+    if (!distinct(d->rows, d->y_sr, 1, 0, 1, 0, d->width) ||
+        (residual_out && !distinct(d->rows, d->resout_sr, 1, 0, 1, 0, d->width)) ||
+        (residual_out && residual_out == residual && d->rows > 1 && d->res_sr != d->resout_sr))
+        return MS_ERR_STRIDE;
     ms::ResidualNormArgs a = residual_args(d, weight, channel_scale, dev_status);
     a.x = x; a.res = residual; a.y = y; a.res_out = residual_out;
     return cuda_rc(ms::launch_residual_norm(a, d->dtype == MS_BF16, d->res_dtype == MS_BF16, false, num_sms_current(),

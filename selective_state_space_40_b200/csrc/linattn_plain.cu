@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kPThr) linattn_plain_kernel(const LaArgs a) {
                 S[i] = decayed(S[i], pre, ys[t][i] * zt);
                 acc = fmaf(xs[t][i], S[i], acc);
             }
-            if (live) {
+            if (live && MS_CHECK(a.status, tok >= 0 && row0 + tok < (a.seq_start ? a.total : a.seqlen) && b < a.batch)) {
                 const int64_t at = o0 + tok * p.o_sl + e;
                 if (p.o_f32) static_cast<float *>(p.o)[at] = p.ro * acc;
                 else Elem<T>::store(static_cast<T *>(p.o) + at, p.ro * acc);
@@ -137,12 +137,16 @@ __global__ void __launch_bounds__(256) linattn_reduce_kernel(const LaReduceArgs 
     if (y >= rpb) return;
     int64_t first = 0, rows = a.batch * a.seqlen;
     if (a.seq_start) {
-        const int64_t s = a.seq_start[0], e = a.seq_start[a.batch];
-        first = s < 0 ? 0 : s;
-        rows = (e < a.total ? e : a.total) - first;
+        // the rows of the sequences that lie in [0, total]: offsets do not decrease
+        int64_t lo = 0, hi = a.batch;
+        while (lo < hi && a.seq_start[lo] < 0) ++lo;
+        while (hi > lo && a.seq_start[hi] > a.total) --hi;
+        first = lo < hi ? a.seq_start[lo] : 0;
+        rows = lo < hi ? a.seq_start[hi] - first : 0;
     }
     for (int64_t r = (int64_t)blockIdx.x * rpb + y; r < rows; r += (int64_t)gridDim.x * rpb) {
         const int64_t row = first + r;
+        if (!MS_CHECK(a.status, row >= 0 && row < (a.seq_start ? a.total : a.batch * a.seqlen))) break;
         const int64_t b = a.seq_start ? 0 : row / a.seqlen, t = a.seq_start ? row : row - b * a.seqlen;
         T *out = static_cast<T *>(a.out) + b * a.o_sb + t * a.o_sl;
         const float *part = a.part + row * a.H * a.d;
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kUThr) linattn_update_kernel(const LaUpdateArg
     const T *k = static_cast<const T *>(a.k) + b * a.k_sb + g * a.k_sh;
     const T *v = static_cast<const T *>(a.v) + b * a.v_sb + g * a.v_sh;
     float *st = a.state + b * a.st_sb + h * a.st_sh + e0;
-    const bool live = e0 < a.dv;
+    const bool live = e0 < a.dv && MS_CHECK(a.status, b < a.batch && e0 + VEC <= a.dv);
     float s[kURows][VEC], acc[VEC], vv[VEC];
     auto fetch = [&](int i0, int end) {
 #pragma unroll

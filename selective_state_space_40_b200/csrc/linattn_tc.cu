@@ -416,6 +416,27 @@ struct Finder {
     }
 };
 
+// (0 * -inf must be 0; NaN stays)
+__device__ __forceinline__ float log_decay_of(const TcArgs &a, int h) {
+    const float g = __ldg(a.log_decay + h);
+    return g < -1e30f ? -1e30f : g;
+}
+
+// What an item may touch lies inside the arrays: its rows, its place among them, its slot of states.
+template <bool kOwn>
+__device__ bool item_ok(const TcArgs &a, const Item &it) {
+    if (it.pi < 0 || it.pi >= a.np || it.zb < 0 || it.zb >= a.p[it.pi].nzb || it.seq < 0 || it.seq >= a.batch || it.h < 0 ||
+        it.h >= a.H || it.nc < 0 || it.j < 0 || it.j >= it.ng)
+        return false;
+    const int slots = a.seq_start ? a.total / a.seg + a.batch : a.batch * a.nseg;
+    if (kOwn && (it.slot0 < 0 || it.slot0 + it.ng > slots)) return false;
+    if (it.nc == 0) return true;
+    const int part = it.cpart >= 0 ? it.npart : kC, steps = (it.nc - 1) * kC;
+    const int lo = a.p[it.pi].rev ? it.row0 - steps : it.row0;
+    const int hi = a.p[it.pi].rev ? it.row0 + part : it.row0 + steps + part;
+    return lo >= 0 && hi <= (a.seq_start ? a.total : a.seqlen);
+}
+
 // The roles' code is what the SM's instruction cache has to hold at once (five
 // groups of warps, each in a loop of its own): with the loops unrolled and the
 // call's parameters read inside them, warps waited for instructions half of the
@@ -514,13 +535,13 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
             }
             Item it;
             const bool valid = finder.find(a, ticket, lane, it);
-            it.valid = valid ? 1 : 0;
+            it.valid = valid && MS_CHECK(a.status, item_ok<kOwn>(a, it)) ? 1 : 0;
             if (i >= 2) ok = __all_sync(0xffffffffu, wait(kBarItemFree + (i & 1), (i >> 1) - 1)) != 0;
             if (!ok) break;
             if (valid) {
                 const TcProblem &p = a.p[it.pi];
                 float *tab = tabs + (i & 1) * M::kTab;
-                const float g = fmaxf(__ldg(a.log_decay + it.h), -1e30f);  // -inf: 0 * -inf must be 0
+                const float g = log_decay_of(a, it.h);
                 for (int k = lane; k <= kC; k += 32) tab[M::kPw + k] = expf((float)k * g);
                 const float w = p.ps * expf((float)lane * g);
                 tab[M::kDiag + 31 + lane] = p.rev && lane > 0 ? 0.0f : w;
@@ -893,7 +914,7 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
             const bool rev = p.rev != 0;
             const int nc = it.nc, cpart = it.cpart, col0 = kZ * it.zb + c0;
             const int64_t blk = p.dx * (int64_t)p.dz, hb = (int64_t)it.h * blk, sb = a.H * blk;
-            const float g = fmaxf(__ldg(a.log_decay + it.h), -1e30f);
+            const float g = log_decay_of(a, it.h);
             const int chain = (it.seq * a.H + it.h) * a.units + it.unit;
             f2 S[NCOL / 2];
 #pragma unroll

@@ -172,6 +172,7 @@ struct LaReduceArgs {
     const float *part;
     void *out;
     const int32_t *seq_start;
+    int *status;
     int64_t batch, seqlen, total, H, kv, d;
     int64_t o_sb, o_sl, o_sh;
 };

@@ -251,7 +251,7 @@ __global__ void __maxnreg__(regs_of(NV, false)) gated_norm_fwd_kernel(const Gate
     float w[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        in[j] = p.live && p.c0 + j * dc < pl.W;
+        in[j] = p.live && p.c0 + j * dc < pl.W && MS_CHECK(a.status, col + j * dc + VEC <= a.width);
         weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], w[j]);
     }
     Raw<T, VEC> rx[NV], rz[NV], nx[NV], nz[NV];
@@ -342,7 +342,7 @@ __global__ void __maxnreg__(regs_of(NV, true)) gated_norm_bwd_kernel(const Gated
     float dw[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        in[j] = p.live && p.c0 + j * dc < pl.W;
+        in[j] = p.live && p.c0 + j * dc < pl.W && MS_CHECK(a.status, col + j * dc + VEC <= a.width);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) dw[j][i] = 0.0f;
     }
@@ -482,7 +482,7 @@ __global__ void __maxnreg__(regs_of(NV, false)) residual_norm_fwd_kernel(const R
     const int dc = pl.tpr * VEC;
     bool in[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) in[j] = p.c0 + j * dc < pl.W;
+    for (int j = 0; j < NV; ++j) in[j] = p.c0 + j * dc < pl.W && MS_CHECK(a.status, col + j * dc + VEC <= a.width);
     Raw<T, VEC> rx[NV], nx[NV];
     Raw<R, VEC> rr[NV], nr[NV];
     auto fetch = [&](int64_t r, Raw<T, VEC> (&fx)[NV], Raw<R, VEC> (&fr)[NV]) {
@@ -569,7 +569,7 @@ __global__ void __maxnreg__(regs_of(NV, true)) residual_norm_bwd_kernel(const Re
     float dw[NV][VEC], dch[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        in[j] = p.c0 + j * dc < pl.W;
+        in[j] = p.c0 + j * dc < pl.W && MS_CHECK(a.status, col + j * dc + VEC <= a.width);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) dw[j][i] = dch[j][i] = 0.0f;
     }

@@ -425,3 +425,77 @@ def test_step_state_beyond_32_bit_offsets():
     ref = mb.linattn_state_update(dense, q, k, v, g, x["scale"])
     assert torch.equal(o, ref) and torch.equal(st, dense)
     assert pool[H * dk * dv:H * dk * dv + 1000].abs().max() == 0
+
+
+@pytest.mark.parametrize("starts,lo,hi", [([0, 90, 200, 230], 0, 200), ([-7, 30, 150, 200], 30, 200)])
+def test_shared_heads_rows_of_bad_sequences_stay(starts, lo, hi):
+    """The sum over shared heads leaves rows of a sequence that is left out as they were, too."""
+    x = make(200, 4, 2, 64, 64, BF, 62, n=3)
+    q, k, v, g, do = dev(x, "q", "k", "v", "g", "do")
+    st = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    grads = {m: torch.full_like(t, 7.0) for m, t in (("dq", q), ("dk", k), ("dv", v))}
+    mb.linattn_bwd(q, k, v, g, do, x["scale"], seq_start=st, grads=grads, dev_status=status)
+    assert status.item() == mb.MS_ERR_SHAPE
+    for t in grads.values():
+        assert (t[:lo] == 7.0).all() and (t[hi:] == 7.0).all() and (t[lo:hi] != 7.0).float().mean() > 0.9
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_broadcast_inputs(dtype):
+    """Keys, values and the gradient of o that rows or tokens share (stride 0) give what their copies give."""
+    b, L, H, d = 2, 70, 3, 16
+    x = make(L, H, H, d, d, dtype, 63)
+    q, k, v, g, do = dev(x, "q", "k", "v", "g", "do")
+    qb = torch.stack([q, -q])
+    kb, vb = k[None].expand(b, L, H, d), v[:1, :1].expand(b, L, H, d)
+    db = do[None].expand(b, L, H, d)
+    o, fin = mb.linattn_fwd(qb, kb, vb, g)
+    # (copies of bf16 run on the tensor cores, with its roundings)
+    for i, sign in ((0, 1.0), (1, -1.0)):
+        y = dict(x, q=sign * x["q"], v=x["v"][:1, :1].expand(L, H, d))
+        want, fw = layer.linattn(f64(y["q"]), f64(y["k"]), f64(y["v"]), f64(x["g"]), d ** -0.5)
+        mag, _ = layer.linattn(*(np.abs(f64(y[m])) for m in ("q", "k", "v")), f64(x["g"]), d ** -0.5)
+        check(o[i], want, mag, 4 * L + d, dtype is BF, "o")
+    # (of bf16, each way is within 4e-3 of the exact gradients, with roundings of its own: 4e-3 sqrt(2) apart)
+    kc, vc = kb.contiguous(), vb.contiguous()
+    gr, gc = (mb.linattn_bwd(qb, kc, vc, g, t) for t in (db, db.contiguous()))
+    for m in ("dq", "dk", "dv"):
+        a, c = gr[m].double(), gc[m].double()
+        assert ((a - c).norm() / c.norm()).item() <= (6e-3 if dtype is BF else 1e-6)
+    with pytest.raises(mb.MambaScanError):
+        mb.linattn_bwd(qb, kb, vc, g, db)
+
+
+def test_nan_decay_spoils_its_head_only():
+    x = make(300, 2, 2, 64, 64, BF, 64)
+    q, k, v, g = dev(x, "q", "k", "v", "g")
+    g2 = g.clone()
+    g2[1] = float("nan")
+    (o, fin), (o2, fin2) = (mb.linattn_fwd(q[None], k[None], v[None], t) for t in (g, g2))
+    assert torch.equal(o[:, :, 0], o2[:, :, 0]) and torch.equal(fin[:, 0], fin2[:, 0])
+    assert o2[:, 1:, 1].isnan().all() and fin2[:, 1].isnan().all()
+
+
+def test_conveniences_on_another_stream():
+    """Given a stream, what a call allocates belongs to that stream: work queued on the current one may still
+    use memory that was freed there."""
+    x = make(600, 4, 2, 64, 64, BF, 65, n=1)
+    q, k, v, g, do = dev(x, "q", "k", "v", "g", "do")
+    want = mb.linattn_bwd(q[None], k[None], v[None], g, do[None])
+    o, fin = mb.linattn_fwd(q[None], k[None], v[None], g)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    junk = [torch.empty(1 << 24, device=DEV) for _ in range(4)]
+    for t in junk:
+        for _ in range(20):
+            t.normal_()
+    del junk, t
+    got = mb.linattn_bwd(q[None], k[None], v[None], g, do[None], stream=side)
+    o2, fin2 = mb.linattn_fwd(q[None], k[None], v[None], g, stream=side)
+    o3 = mb.linattn_state_update(fin2, q[:1], k[:1], v[:1], g, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2)
+    for m in ("dq", "dk", "dv", "dinitial_state"):
+        assert torch.equal(want[m], got[m])
+    assert torch.equal(o3, mb.linattn_state_update(fin, q[:1], k[:1], v[:1], g)) and torch.equal(fin, fin2)

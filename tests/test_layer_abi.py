@@ -177,3 +177,51 @@ def test_conveniences_refuse_on_the_host():
         mb.residual_norm_fwd(x, weight=torch.zeros(7))
     with pytest.raises(ValueError, match="CUDA"):
         mb.residual_norm_bwd(x, None, x)
+
+
+@pytest.mark.parametrize("kw,fwd,bwd", [
+    (dict(o_sb=0), mb.MS_ERR_STRIDE, None),                  # rows of o written twice
+    (dict(o_sl=0), mb.MS_ERR_STRIDE, None),
+    (dict(o_sh=63), mb.MS_ERR_STRIDE, None),                 # heads overlap by one
+    (dict(q_sb=0), None, mb.MS_ERR_STRIDE),                  # broadcast inputs: not those of the gradients
+    (dict(k_sh=0), None, mb.MS_ERR_STRIDE),
+    (dict(v_sl=0), None, mb.MS_ERR_STRIDE),
+    (dict(k_sl=64, k_sh=16 * 64), None, None),               # heads outside the tokens
+    (dict(o_sb=64, o_sl=128, o_sh=16 * 128), None, None),    # batch inside the tokens
+    (dict(batch=1, q_sb=0, o_sb=0), None, None),             # one row: its stride is not used
+    (dict(kv_heads=1, k_sh=0, v_sh=0), None, None),
+])
+def test_written_arrays_hold_no_element_twice(kw, fwd, bwd):
+    # the workspace check comes behind the strides' one: the calls end there at the latest
+    d = _dims(**kw)
+    assert _bwd(d) == (bwd or mb.MS_ERR_WORKSPACE)
+    assert _fwd(d, o=FAKE + 1) == (fwd or mb.MS_ERR_ALIGN)
+
+
+def test_outputs_that_are_inputs_are_refused():
+    d = _dims(kv_heads=4, k_sb=4096, k_sl=256, v_sb=4096, v_sl=256)
+    need = max(mb.mamba_linattn_bwd_workspace_size(d, False), mb.mamba_linattn_workspace_size(d, False))
+    at = [FAKE + (i << 12) for i in range(12)]
+    for o in at[:3]:
+        assert mb.mamba_linattn_fwd(*at[:3], at[3], 1.0, None, None, o, None, d, at[9], need, None, None) == mb.MS_ERR_SHAPE
+    back = lambda grads, s0=None, ds0=None: mb.mamba_linattn_bwd(  # noqa: E731
+        *at[:3], at[3], 1.0, None, s0, at[4], None, *grads, ds0, d, at[9], need, None, None)
+    for bad in (at[0], at[1], at[2], at[4]):
+        assert back((bad, at[6], at[7])) == back((at[5], bad, at[7])) == back((at[5], at[6], bad)) == mb.MS_ERR_SHAPE
+    assert back((at[5], at[5], at[7])) == back((at[5], at[6], at[6])) == back((at[5], at[6], at[5])) == mb.MS_ERR_SHAPE
+    assert back(at[5:8], at[8], at[8]) == mb.MS_ERR_SHAPE
+
+
+def test_norms_refuse_rows_written_twice():
+    g = dict(rows=4, width=64, groups=2, x_sr=0, z_sr=0, y_sr=63, eps=1e-5, dtype=mb.MS_BF16, gate_first=0)
+    assert mb.mamba_gated_norm_fwd(FAKE, FAKE, None, FAKE, mb.GatedNormDims(**g), None, None) == mb.MS_ERR_STRIDE
+    r = dict(rows=4, width=64, x_sr=64, res_sr=64, y_sr=64, resout_sr=64, eps=1e-5, res_scale=1.0, dtype=mb.MS_BF16,
+             res_dtype=mb.MS_F32)
+    for kw in (dict(y_sr=0), dict(resout_sr=32), dict(resout_sr=128)):  # the last: in place with another stride
+        d = mb.ResidualNormDims(**dict(r, **kw))
+        assert mb.mamba_residual_norm_fwd(FAKE, FAKE, None, None, FAKE, FAKE, d, None, None) == mb.MS_ERR_STRIDE
+    u = dict(batch=3, nheads=4, kv_heads=2, dk=64, dv=64, q_sb=256, q_sh=64, k_sb=128, k_sh=64, v_sb=128, v_sh=64,
+             o_sb=256, o_sh=64, state_sb=4 * 4096, state_sh=4096, dtype=mb.MS_F32)
+    for kw in (dict(o_sb=0), dict(o_sh=0), dict(state_sb=4096, state_sh=4096)):
+        d = mb.LinattnUpdateDims(**dict(u, **kw))
+        assert mb.mamba_linattn_state_update(FAKE, FAKE, FAKE, FAKE, FAKE, 1.0, FAKE, d, None, None) == mb.MS_ERR_STRIDE
