@@ -9,7 +9,7 @@
 // Both passes hold their row in registers between the sum and the use of it,
 // so every array crosses HBM once, which is what bounds them. A group is held
 // by tpr threads, NV vectors of VEC neighbouring columns each (16 bytes of the
-// inputs' type where every row allows it, else single columns); the sums go
+// inputs' type where every row allows it, else loaded column by column); the sums go
 // over the threads by shuffles, and over the warps through shared memory where
 // a group has more than one. A block is a column block of gb groups times ty
 // rows and walks down the rows, so a thread's columns, and the weights' sums
@@ -35,15 +35,15 @@ constexpr int kMaxThr = 640;  // threads of a block, at most
 constexpr int regs_of(int nv, bool bwd) { return nv > 1 || bwd ? 96 : 56; }
 
 // VEC neighbouring elements as they lie in memory: a row waits in this form.
-template <typename T, int VEC>
+template <typename T, int VEC, bool ODD>
 struct Raw {
     uint4 v[VEC * sizeof(T) / 16];
-    __device__ __forceinline__ void load(const T *p, bool on) {
+    __device__ __forceinline__ void load(const T *p, int on) {
 #pragma unroll
         for (int q = 0; q < (int)(VEC * sizeof(T) / 16); ++q)
             v[q] = on ? __ldg(reinterpret_cast<const uint4 *>(p) + q) : make_uint4(0, 0, 0, 0);
     }
-    __device__ __forceinline__ void load_shared(uint32_t at, bool on) {
+    __device__ __forceinline__ void load_shared(uint32_t at, int on) {
 #pragma unroll
         for (int q = 0; q < (int)(VEC * sizeof(T) / 16); ++q) {
             v[q] = make_uint4(0, 0, 0, 0);
@@ -70,28 +70,36 @@ struct Raw {
         }
     }
 };
-template <typename T>
-struct Raw<T, 1> {
-    float v;
-    __device__ __forceinline__ void load(const T *p, bool on) { v = on ? Elem<T>::load(p) : 0.0f; }
-    __device__ __forceinline__ void load_shared(uint32_t, bool) {}  // (rings carry whole vectors)
-    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = v; }
+// The same column by column, for rows of any alignment and width: `on` is how many there are.
+template <typename T, int VEC>
+struct Raw<T, VEC, true> {
+    float v[VEC];
+    __device__ __forceinline__ void load(const T *p, int on) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = i < on ? Elem<T>::load(p + i) : 0.0f;
+    }
+    __device__ __forceinline__ void get(float (&f)[VEC]) const {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[i] = v[i];
+    }
 };
 // fp32 weights of VEC columns, 1 where there are none
-template <int VEC>
-__device__ __forceinline__ void weights(const float *w, bool on, float (&f)[VEC]) {
+template <int VEC, bool ODD>
+__device__ __forceinline__ void weights(const float *w, int on, float (&f)[VEC]) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) f[i] = 1.0f;
     if (w && on) {
-        Raw<float, VEC> r;
-        r.load(w, true);
+        Raw<float, VEC, ODD> r;
+        r.load(w, on);
         r.get(f);
     }
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC]) {
-    if constexpr (VEC == 1) {
-        Elem<T>::store(p, v[0]);
+template <typename T, int VEC, bool ODD>
+__device__ __forceinline__ void store_vec(T *p, const float (&v)[VEC], int on) {
+    if constexpr (ODD) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (i < on) Elem<T>::store(p + i, v[i]);
     } else if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int q = 0; q < VEC / 8; ++q) {
@@ -236,30 +244,42 @@ __device__ __forceinline__ float sigmoid_f(float z) { return rcp_mufu(1.0f + exp
 
 // The rows of a block are read one ahead of the row in work where the registers
 // allow it: a row's sums wait for all of its columns.
+// How rows come: straight to registers, through a ring in shared memory, or straight and column by column
+// (rows that 16-byte accesses do not fit).
+enum { kStraight = 0, kRing = 1, kOdd = 2 };
+template <int VEC>
+__device__ __forceinline__ int columns(int left) {
+    return left <= 0 ? 0 : left < VEC ? left : VEC;
+}
+
 template <int VEC, int NV, bool RING>
 constexpr bool kAhead = !RING && VEC *NV <= 16;
+template <int VEC, int NV, bool RING>
+constexpr bool kAheadBwd = !RING && VEC *NV <= 4;
 
-template <typename T, int VEC, int NV, bool RING, int GATE>
+template <typename T, int VEC, int NV, int ROWS, int GATE>
 __global__ void __maxnreg__(regs_of(NV, false)) gated_norm_fwd_kernel(const GatedNormArgs a, const NormPlan pl) {
+    constexpr bool RING = ROWS == kRing, ODD = ROWS == kOdd;
     __shared__ float sm[2][2 * kMaxWarps];
     int turn = 0;
     const Place p = place_of<VEC>(pl, a.groups);
     const float invW = 1.0f / (float)pl.W;
     const int64_t col = p.g * pl.W + p.c0, dr = (int64_t)gridDim.x * pl.ty;
     const int dc = pl.tpr * VEC;
-    bool in[NV];
+    int in[NV];  // columns of each vector that there are
     float w[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        in[j] = p.live && p.c0 + j * dc < pl.W && MS_CHECK(a.status, col + j * dc + VEC <= a.width);
-        weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], w[j]);
+        in[j] = p.live ? columns<VEC>(pl.W - p.c0 - j * dc) : 0;
+        if (!MS_CHECK(a.status, in[j] == 0 || col + j * dc + in[j] <= a.width)) in[j] = 0;
+        weights<VEC, ODD>(a.w ? a.w + col + j * dc : nullptr, in[j], w[j]);
     }
-    Raw<T, VEC> rx[NV], rz[NV], nx[NV], nz[NV];
+    Raw<T, VEC, ODD> rx[NV], rz[NV], nx[NV], nz[NV];
     const T *x = static_cast<const T *>(a.x) + col, *z = static_cast<const T *>(a.z) + col;
-    auto fetch = [&](int64_t r, Raw<T, VEC> (&fx)[NV], Raw<T, VEC> (&fz)[NV]) {
+    auto fetch = [&](int64_t r, Raw<T, VEC, ODD> (&fx)[NV], Raw<T, VEC, ODD> (&fz)[NV]) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool on = in[j] && r < a.rows;
+            const int on = r < a.rows ? in[j] : 0;
             fx[j].load(x + r * a.x_sr + j * dc, on);
             if constexpr (GATE != kNoGate) fz[j].load(z + r * a.z_sr + j * dc, on);
         }
@@ -324,42 +344,52 @@ __global__ void __maxnreg__(regs_of(NV, false)) gated_norm_fwd_kernel(const Gate
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) v[j][i] *= silu_f(g[i]);
             }
-            if (in[j] && r < a.rows) store_vec<T, VEC>(static_cast<T *>(a.y) + r * a.y_sr + col + j * dc, v[j]);
+            if (in[j] && r < a.rows) store_vec<T, VEC, ODD>(static_cast<T *>(a.y) + r * a.y_sr + col + j * dc, v[j], in[j]);
             if (kAhead<VEC, NV, RING>) rx[j] = nx[j], rz[j] = nz[j];
         }
     }
 }
 
-template <typename T, int VEC, int NV, bool RING, int GATE>
+template <typename T, int VEC, int NV, int ROWS, int GATE>
 __global__ void __maxnreg__(regs_of(NV, true)) gated_norm_bwd_kernel(const GatedNormArgs a, const NormPlan pl) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr bool RING = ROWS == kRing, ODD = ROWS == kOdd;
     __shared__ float sm[2][2 * kMaxWarps];
     int turn = 0;
     const Place p = place_of<VEC>(pl, a.groups);
     const float invW = 1.0f / (float)pl.W;
     const int64_t col = p.g * pl.W + p.c0, dr = (int64_t)gridDim.x * pl.ty;
     const int dc = pl.tpr * VEC;
-    bool in[NV];
+    int in[NV];  // columns of each vector that there are
     float dw[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        in[j] = p.live && p.c0 + j * dc < pl.W && MS_CHECK(a.status, col + j * dc + VEC <= a.width);
+        in[j] = p.live ? columns<VEC>(pl.W - p.c0 - j * dc) : 0;
+        if (!MS_CHECK(a.status, in[j] == 0 || col + j * dc + in[j] <= a.width)) in[j] = 0;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) dw[j][i] = 0.0f;
     }
-    Raw<T, VEC> rx[NV], rz[NV], ry[NV];
+    constexpr bool kAh = kAheadBwd<VEC, NV, RING>;
+    Raw<T, VEC, ODD> rx[NV], rz[NV], ry[NV], nx[kAh ? NV : 1], nz[kAh ? NV : 1], ny[kAh ? NV : 1];
     const T *x = static_cast<const T *>(a.x) + col, *z = static_cast<const T *>(a.z) + col;
     const T *dy = static_cast<const T *>(a.dy) + col;
+    auto fetch = [&](int64_t r, int j, Raw<T, VEC, ODD> &fx, Raw<T, VEC, ODD> &fy, Raw<T, VEC, ODD> &fz) {
+        const int on = r < a.rows ? in[j] : 0;
+        fx.load(x + r * a.x_sr + j * dc, on);
+        fy.load(dy + r * a.y_sr + j * dc, on);
+        if constexpr (GATE != kNoGate) fz.load(z + r * a.z_sr + j * dc, on);
+    };
     const float *wt = a.w ? a.w + col : nullptr;
     float hw[kHold<VEC, NV> ? NV : 1][VEC];
     if constexpr (kHold<VEC, NV>)
 #pragma unroll
-        for (int j = 0; j < NV; ++j) weights<VEC>(wt ? wt + j * dc : nullptr, in[j], hw[j]);
+        for (int j = 0; j < NV; ++j) weights<VEC, ODD>(wt ? wt + j * dc : nullptr, in[j], hw[j]);
     auto weights_of = [&](int j, float (&w)[VEC]) {
         if constexpr (kHold<VEC, NV>) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) w[i] = hw[j][i];
         } else {
-            weights<VEC>(wt ? wt + j * dc : nullptr, in[j], w);
+            weights<VEC, ODD>(wt ? wt + j * dc : nullptr, in[j], w);
         }
     };
     extern __shared__ __align__(128) unsigned char ring_smem[];
@@ -381,22 +411,25 @@ __global__ void __maxnreg__(regs_of(NV, true)) gated_norm_bwd_kernel(const Gated
                 if (blockIdx.x + i * dr < a.rows) refill(i, blockIdx.x + i * dr);
     }
     int64_t r = (int64_t)blockIdx.x * pl.ty + p.ty;
+    if constexpr (kAh)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) fetch(r, j, rx[j], ry[j], rz[j]);
     for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += dr, r += dr) {
         float s[2] = {0.0f, 0.0f};
         if constexpr (RING) ring.wait(st, phase, a.status);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool on = in[j] && r < a.rows;
             if constexpr (RING) {
+                const int on = r < a.rows ? in[j] : 0;
                 const uint32_t at = (p.c0 + j * dc) * (uint32_t)sizeof(T);
                 rx[j].load_shared(ring.row(st, 0) + at, on);
                 ry[j].load_shared(ring.row(st, 1) + at, on);
                 if constexpr (GATE != kNoGate) rz[j].load_shared(ring.row(st, 2) + at, on);
-                continue;
+            } else if constexpr (kAh) {
+                fetch(r + dr, j, nx[j], ny[j], nz[j]);
+            } else {
+                fetch(r, j, rx[j], ry[j], rz[j]);
             }
-            rx[j].load(x + r * a.x_sr + j * dc, on);
-            ry[j].load(dy + r * a.y_sr + j * dc, on);
-            if constexpr (GATE != kNoGate) rz[j].load(z + r * a.z_sr + j * dc, on);
         }
         // u: the normed value; gr: the gradient of n(u) w; sig: silu(z) = z sig, of which both
         // passes need, kept between them (the formulas' instructions, not HBM, bound this kernel)
@@ -459,38 +492,43 @@ __global__ void __maxnreg__(regs_of(NV, true)) gated_norm_bwd_kernel(const Gated
                 }
             }
             if (in[j] && r < a.rows) {
-                store_vec<T, VEC>(static_cast<T *>(a.dx) + r * a.width + col + j * dc, u);
-                if constexpr (GATE != kNoGate) store_vec<T, VEC>(static_cast<T *>(a.dz) + r * a.width + col + j * dc, dz);
+                store_vec<T, VEC, ODD>(static_cast<T *>(a.dx) + r * a.width + col + j * dc, u, in[j]);
+                if constexpr (GATE != kNoGate) store_vec<T, VEC, ODD>(static_cast<T *>(a.dz) + r * a.width + col + j * dc, dz, in[j]);
             }
+            if constexpr (kAh) rx[j] = nx[j], ry[j] = ny[j], rz[j] = nz[j];
         }
     }
     if (a.dw) {
         float *part = a.part + ((int64_t)blockIdx.x * pl.ty + p.ty) * a.width + col;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (in[j]) store_vec<float, VEC>(part + j * dc, dw[j]);
+            if (in[j]) store_vec<float, VEC, ODD>(part + j * dc, dw[j], in[j]);
     }
 }
 
-template <typename T, typename R, int VEC, int NV, bool RING>
+template <typename T, typename R, int VEC, int NV, int ROWS>
 __global__ void __maxnreg__(regs_of(NV, false)) residual_norm_fwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
+    constexpr bool RING = ROWS == kRing, ODD = ROWS == kOdd;
     __shared__ float sm[2][2 * kMaxWarps];
     int turn = 0;
     const Place p = place_of<VEC>(pl, 1);
     const float invW = 1.0f / (float)pl.W;
     const int64_t col = p.c0, dr = (int64_t)gridDim.x * pl.ty;
     const int dc = pl.tpr * VEC;
-    bool in[NV];
+    int in[NV];  // columns of each vector that there are
 #pragma unroll
-    for (int j = 0; j < NV; ++j) in[j] = p.c0 + j * dc < pl.W && MS_CHECK(a.status, col + j * dc + VEC <= a.width);
-    Raw<T, VEC> rx[NV], nx[NV];
-    Raw<R, VEC> rr[NV], nr[NV];
-    auto fetch = [&](int64_t r, Raw<T, VEC> (&fx)[NV], Raw<R, VEC> (&fr)[NV]) {
+    for (int j = 0; j < NV; ++j) {
+        in[j] = columns<VEC>(pl.W - p.c0 - j * dc);
+        if (!MS_CHECK(a.status, in[j] == 0 || col + j * dc + in[j] <= a.width)) in[j] = 0;
+    }
+    Raw<T, VEC, ODD> rx[NV], nx[NV];
+    Raw<R, VEC, ODD> rr[NV], nr[NV];
+    auto fetch = [&](int64_t r, Raw<T, VEC, ODD> (&fx)[NV], Raw<R, VEC, ODD> (&fr)[NV]) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool on = in[j] && r < a.rows;
+            const int on = r < a.rows ? in[j] : 0;
             fx[j].load(static_cast<const T *>(a.x) + r * a.x_sr + col + j * dc, on);
-            fr[j].load(static_cast<const R *>(a.res) + r * a.res_sr + col + j * dc, on && a.res);
+            fr[j].load(static_cast<const R *>(a.res) + r * a.res_sr + col + j * dc, a.res ? on : 0);
         }
     };
     extern __shared__ __align__(128) unsigned char ring_smem[];
@@ -520,7 +558,7 @@ __global__ void __maxnreg__(regs_of(NV, false)) residual_norm_fwd_kernel(const R
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 rx[j].load_shared(ring.row(st, 0) + (p.c0 + j * dc) * (uint32_t)sizeof(T), in[j]);
-                rr[j].load_shared(ring.row(st, 1) + (p.c0 + j * dc) * (uint32_t)sizeof(R), in[j] && a.res);
+                rr[j].load_shared(ring.row(st, 1) + (p.c0 + j * dc) * (uint32_t)sizeof(R), a.res ? in[j] : 0);
             }
         }
         float h[NV][VEC], s[1] = {0.0f};
@@ -529,14 +567,14 @@ __global__ void __maxnreg__(regs_of(NV, false)) residual_norm_fwd_kernel(const R
             float x[VEC], c[VEC];
             rx[j].get(x);
             rr[j].get(h[j]);
-            weights<VEC>(a.cs ? a.cs + col + j * dc : nullptr, in[j], c);
+            weights<VEC, ODD>(a.cs ? a.cs + col + j * dc : nullptr, in[j], c);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) {
                 h[j][i] = fmaf(a.scale * c[i], x[i], h[j][i]);
                 s[0] = fmaf(h[j][i], h[j][i], s[0]);
             }
             if (in[j] && r < a.rows && a.res_out)
-                store_vec<R, VEC>(static_cast<R *>(a.res_out) + r * a.ro_sr + col + j * dc, h[j]);
+                store_vec<R, VEC, ODD>(static_cast<R *>(a.res_out) + r * a.ro_sr + col + j * dc, h[j], in[j]);
         }
         group_sum<1>(s, pl.tpr, sm, turn);
         if constexpr (RING) {
@@ -548,28 +586,31 @@ __global__ void __maxnreg__(regs_of(NV, false)) residual_norm_fwd_kernel(const R
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             float w[VEC];
-            weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], w);
+            weights<VEC, ODD>(a.w ? a.w + col + j * dc : nullptr, in[j], w);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) h[j][i] *= inv * w[i];
-            if (in[j] && r < a.rows) store_vec<T, VEC>(static_cast<T *>(a.y) + r * a.y_sr + col + j * dc, h[j]);
+            if (in[j] && r < a.rows) store_vec<T, VEC, ODD>(static_cast<T *>(a.y) + r * a.y_sr + col + j * dc, h[j], in[j]);
             if (kAhead<VEC, NV, RING>) rx[j] = nx[j], rr[j] = nr[j];
         }
     }
 }
 
-template <typename T, typename R, int VEC, int NV, bool RING>
+template <typename T, typename R, int VEC, int NV, int ROWS>
 __global__ void __maxnreg__(regs_of(NV, true)) residual_norm_bwd_kernel(const ResidualNormArgs a, const NormPlan pl) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr bool RING = ROWS == kRing, ODD = ROWS == kOdd;
     __shared__ float sm[2][2 * kMaxWarps];
     int turn = 0;
     const Place p = place_of<VEC>(pl, 1);
     const float invW = 1.0f / (float)pl.W;
     const int64_t col = p.c0, dr = (int64_t)gridDim.x * pl.ty;
     const int dc = pl.tpr * VEC;
-    bool in[NV];
+    int in[NV];  // columns of each vector that there are
     float dw[NV][VEC], dch[NV][VEC];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        in[j] = p.c0 + j * dc < pl.W && MS_CHECK(a.status, col + j * dc + VEC <= a.width);
+        in[j] = columns<VEC>(pl.W - p.c0 - j * dc);
+        if (!MS_CHECK(a.status, in[j] == 0 || col + j * dc + in[j] <= a.width)) in[j] = 0;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) dw[j][i] = dch[j][i] = 0.0f;
     }
@@ -577,19 +618,27 @@ __global__ void __maxnreg__(regs_of(NV, true)) residual_norm_bwd_kernel(const Re
     if constexpr (kHold<VEC, NV>)
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            weights<VEC>(a.w ? a.w + col + j * dc : nullptr, in[j], hw[j]);
-            weights<VEC>(a.cs ? a.cs + col + j * dc : nullptr, in[j], hc[j]);
+            weights<VEC, ODD>(a.w ? a.w + col + j * dc : nullptr, in[j], hw[j]);
+            weights<VEC, ODD>(a.cs ? a.cs + col + j * dc : nullptr, in[j], hc[j]);
         }
     auto weights_of = [&](const float *from, const float (&held)[kHold<VEC, NV> ? NV : 1][VEC], int j, float (&w)[VEC]) {
         if constexpr (kHold<VEC, NV>) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) w[i] = held[j][i];
         } else {
-            weights<VEC>(from ? from + col + j * dc : nullptr, in[j], w);
+            weights<VEC, ODD>(from ? from + col + j * dc : nullptr, in[j], w);
         }
     };
-    Raw<R, VEC> rh[NV], rd[NV];
-    Raw<T, VEC> ry[NV], rx[NV];
+    constexpr bool kAh = kAheadBwd<VEC, NV, RING>;
+    Raw<R, VEC, ODD> rh[NV], rd[NV], nh[kAh ? NV : 1], nd[kAh ? NV : 1];
+    Raw<T, VEC, ODD> ry[NV], rx[NV], ny[kAh ? NV : 1], nx[kAh ? NV : 1];
+    auto fetch = [&](int64_t r, int j, Raw<R, VEC, ODD> &fh, Raw<T, VEC, ODD> &fy, Raw<R, VEC, ODD> &fd, Raw<T, VEC, ODD> &fx) {
+        const int on = r < a.rows ? in[j] : 0;
+        fh.load(static_cast<const R *>(a.res_out) + r * a.ro_sr + col + j * dc, on);
+        fy.load(static_cast<const T *>(a.dy) + r * a.y_sr + col + j * dc, on);
+        fd.load(static_cast<const R *>(a.dres_out) + r * a.res_sr + col + j * dc, a.dres_out ? on : 0);
+        fx.load(static_cast<const T *>(a.x) + r * a.x_sr + col + j * dc, a.dcs ? on : 0);
+    };
     extern __shared__ __align__(128) unsigned char ring_smem[];
     Ring<4> ring;
     int st = 0;  // the row's stage, and its phase
@@ -611,24 +660,26 @@ __global__ void __maxnreg__(regs_of(NV, true)) residual_norm_bwd_kernel(const Re
                 if (blockIdx.x + i * dr < a.rows) refill(i, blockIdx.x + i * dr);
     }
     int64_t r = (int64_t)blockIdx.x * pl.ty + p.ty;
+    if constexpr (kAh)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) fetch(r, j, rh[j], ry[j], rd[j], rx[j]);
     for (int64_t r0 = (int64_t)blockIdx.x * pl.ty; r0 < a.rows; r0 += dr, r += dr) {
         float s[2] = {0.0f, 0.0f};
         if constexpr (RING) ring.wait(st, phase, a.status);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool on = in[j] && r < a.rows;
             if constexpr (RING) {
+                const int on = r < a.rows ? in[j] : 0;
                 const uint32_t at = (p.c0 + j * dc) * (uint32_t)sizeof(T), ar = (p.c0 + j * dc) * (uint32_t)sizeof(R);
                 rh[j].load_shared(ring.row(st, 0) + ar, on);
                 ry[j].load_shared(ring.row(st, 1) + at, on);
-                rd[j].load_shared(ring.row(st, 2) + ar, on && a.dres_out);
-                rx[j].load_shared(ring.row(st, 3) + at, on && a.dcs);
-                continue;
+                rd[j].load_shared(ring.row(st, 2) + ar, a.dres_out ? on : 0);
+                rx[j].load_shared(ring.row(st, 3) + at, a.dcs ? on : 0);
+            } else if constexpr (kAh) {
+                fetch(r + dr, j, nh[j], ny[j], nd[j], nx[j]);
+            } else {
+                fetch(r, j, rh[j], ry[j], rd[j], rx[j]);
             }
-            rh[j].load(static_cast<const R *>(a.res_out) + r * a.ro_sr + col + j * dc, on);
-            ry[j].load(static_cast<const T *>(a.dy) + r * a.y_sr + col + j * dc, on);
-            rd[j].load(static_cast<const R *>(a.dres_out) + r * a.res_sr + col + j * dc, on && a.dres_out);
-            rx[j].load(static_cast<const T *>(a.x) + r * a.x_sr + col + j * dc, on && a.dcs);
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
@@ -666,42 +717,56 @@ __global__ void __maxnreg__(regs_of(NV, true)) residual_norm_bwd_kernel(const Re
                 dch[j][i] = fmaf(a.scale * d[i], x[i], dch[j][i]);
             }
             if (in[j] && r < a.rows) {
-                if (a.dres) store_vec<R, VEC>(static_cast<R *>(a.dres) + r * a.width + col + j * dc, d);
+                if (a.dres) store_vec<R, VEC, ODD>(static_cast<R *>(a.dres) + r * a.width + col + j * dc, d, in[j]);
 #pragma unroll
                 for (int i = 0; i < VEC; ++i) d[i] *= a.scale * c[i];
-                if (a.dx) store_vec<T, VEC>(static_cast<T *>(a.dx) + r * a.width + col + j * dc, d);
+                if (a.dx) store_vec<T, VEC, ODD>(static_cast<T *>(a.dx) + r * a.width + col + j * dc, d, in[j]);
             }
+            if constexpr (kAh) rh[j] = nh[j], ry[j] = ny[j], rd[j] = nd[j], rx[j] = nx[j];
         }
     }
     const int64_t prow = (int64_t)blockIdx.x * pl.ty + p.ty, parts = (int64_t)gridDim.x * pl.ty;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (!in[j]) continue;
-        if (a.dw) store_vec<float, VEC>(a.part + prow * a.width + col + j * dc, dw[j]);
-        if (a.dcs) store_vec<float, VEC>(a.part + (parts + prow) * a.width + col + j * dc, dch[j]);
+        if (a.dw) store_vec<float, VEC, ODD>(a.part + prow * a.width + col + j * dc, dw[j], in[j]);
+        if (a.dcs) store_vec<float, VEC, ODD>(a.part + (parts + prow) * a.width + col + j * dc, dch[j], in[j]);
     }
 }
 
-// out[c] = sum over the rows of part, each thread its own rows in order and then
-// the threads of a column in order. Latency bounds it: 32 threads share a column.
-constexpr int kSumRows = 32;
-__global__ void __launch_bounds__(32 * kSumRows) norm_sum_kernel(const float *part, float *out0, float *out1, int64_t parts,
-                                                                 int64_t width) {
-    __shared__ float sm[kSumRows][33];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + tx;
+// out[c] = sum over the rows of part: each thread its own rows in order, then the threads
+// of a column in order. Latency bounds it: 1024 threads share CW columns.
+constexpr int kSumThr = 1024;
+template <int CW>
+__global__ void __launch_bounds__(kSumThr) norm_sum_kernel(const float *part, float *out0, float *out1, int64_t parts,
+                                                           int64_t width) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums are there
+    constexpr int TY = kSumThr / CW, T2 = 16;
+    __shared__ float sm[TY][CW + 1];
+    const int tx = threadIdx.x % CW, ty = threadIdx.x / CW;
+    const int64_t c = (int64_t)blockIdx.x * CW + tx;
     float *out = blockIdx.y ? out1 : out0;
     if (out == nullptr) return;
     const float *src = part + (int64_t)blockIdx.y * parts * width;
     float s = 0.0f;
     if (c < width) {
 #pragma unroll 8
-        for (int64_t r = ty; r < parts; r += kSumRows) s += src[r * width + c];
+        for (int64_t r = ty; r < parts; r += TY) s += src[r * width + c];
     }
     sm[ty][tx] = s;
     __syncthreads();
+    if (ty < T2) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < TY / T2; ++i) s += sm[ty * (TY / T2) + i][tx];
+    }
+    __syncthreads();
+    if (ty < T2) sm[ty][tx] = s;
+    __syncthreads();
     if (ty == 0 && c < width) {
-        for (int i = 1; i < kSumRows; ++i) s += sm[i][tx];
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < T2; ++i) s += sm[i][tx];
         out[c] = s;
     }
 }
@@ -715,11 +780,14 @@ int threads_for(int64_t W, int vec, int nv) {
     return t;
 }
 
-// Vectors per thread: the fewest that keep a group within a block.
-int vectors_for(int64_t W, int vec) {
-    for (int nv = 1; nv < 32; nv *= 2)
-        if (threads_for(W, vec, nv) <= kMaxThr) return nv;
-    return 32;
+// Vectors per thread: the fewest that keep a group within a block (16384 columns in fours: 8). Rows that
+// come column by column take smaller blocks, more of which have a row on its way, in the backward and where
+// a thread has two vectors in any case (8000 rows, bf16: residual backward, 1503 columns 68 us, 119 us with
+// 384 threads; gated forward, 4001 columns 114 and 135; but residual forward, 1503 columns 51 and 46).
+int vectors_for(int64_t W, int vec, bool odd, bool bwd) {
+    int nv = 1;
+    while (nv < 8 && threads_for(W, vec, nv) > (odd && (bwd || nv > 1) ? kMaxThr / 2 : kMaxThr)) nv *= 2;
+    return nv;
 }
 
 NormPlan plan_norm(int64_t rows, int64_t W, int64_t groups, int vec, int nv, int num_sms, bool bwd) {
@@ -751,8 +819,8 @@ NormPlan plan_norm(int64_t rows, int64_t W, int64_t groups, int vec, int nv, int
 // A ring of rows pays where a block works down several of them and a group fills more than
 // a warp; its blocks share the SM's shared memory.
 constexpr int kMaxSmem = 220 * 1024;
-void add_ring(NormPlan &pl, int64_t rows, int vec, size_t row_bytes, int num_sms) {
-    if (vec == 1 || pl.tpr <= 32 || rows < 3 * (int64_t)pl.rblocks) return;
+void add_ring(NormPlan &pl, int64_t rows, bool odd, size_t row_bytes, int num_sms) {
+    if (odd || pl.tpr <= 32 || rows < 3 * (int64_t)pl.rblocks) return;
     const int64_t per_sm = std::max<int64_t>(1, ((int64_t)pl.rblocks * pl.gblocks + num_sms - 1) / num_sms);
     const int64_t n = (kMaxSmem / per_sm - 1024 - 128) / (int64_t)row_bytes;
     pl.stages = (int)std::min<int64_t>(n, 8);
@@ -773,50 +841,63 @@ cudaError_t launch(K kernel, const A &a, const NormPlan &pl, size_t row_bytes, S
     kernel<<<dim3((unsigned)pl.rblocks, (unsigned)pl.gblocks), (unsigned)(pl.tpr * pl.gb * pl.ty), smem, st>>>(a, pl);
     return cudaGetLastError();
 }
-template <int NV, typename T, int VEC, int GATE>
+template <int NV, typename T, int VEC, int GATE, bool ODD>
 cudaError_t run_gate(const GatedNormArgs &a, const NormPlan &pl, size_t row_bytes, bool bwd, cudaStream_t st) {
     static SmemOptIn opt_in[2];
-    if constexpr (VEC > 1)
+    if constexpr (!ODD)
         if (pl.stages)
-            return bwd ? launch(gated_norm_bwd_kernel<T, VEC, NV, true, GATE>, a, pl, row_bytes, opt_in[1], st)
-                       : launch(gated_norm_fwd_kernel<T, VEC, NV, true, GATE>, a, pl, row_bytes, opt_in[0], st);
-    return bwd ? launch(gated_norm_bwd_kernel<T, VEC, NV, false, GATE>, a, pl, 0, opt_in[1], st)
-               : launch(gated_norm_fwd_kernel<T, VEC, NV, false, GATE>, a, pl, 0, opt_in[0], st);
+            return bwd ? launch(gated_norm_bwd_kernel<T, VEC, NV, kRing, GATE>, a, pl, row_bytes, opt_in[1], st)
+                       : launch(gated_norm_fwd_kernel<T, VEC, NV, kRing, GATE>, a, pl, row_bytes, opt_in[0], st);
+    constexpr int ROWS = ODD ? kOdd : kStraight;
+    return bwd ? launch(gated_norm_bwd_kernel<T, VEC, NV, ROWS, GATE>, a, pl, 0, opt_in[1], st)
+               : launch(gated_norm_fwd_kernel<T, VEC, NV, ROWS, GATE>, a, pl, 0, opt_in[0], st);
 }
-template <int NV, typename T, int VEC>
+template <int NV, typename T, int VEC, bool ODD>
 cudaError_t run_gated(const GatedNormArgs &a, const NormPlan &pl, size_t row_bytes, bool bwd, cudaStream_t st) {
-    if (!a.z) return run_gate<NV, T, VEC, kNoGate>(a, pl, row_bytes, bwd, st);
-    return a.gate_first ? run_gate<NV, T, VEC, kGateFirst>(a, pl, row_bytes, bwd, st)
-                        : run_gate<NV, T, VEC, kGateBehind>(a, pl, row_bytes, bwd, st);
+    if (!a.z) return run_gate<NV, T, VEC, kNoGate, ODD>(a, pl, row_bytes, bwd, st);
+    return a.gate_first ? run_gate<NV, T, VEC, kGateFirst, ODD>(a, pl, row_bytes, bwd, st)
+                        : run_gate<NV, T, VEC, kGateBehind, ODD>(a, pl, row_bytes, bwd, st);
 }
-template <int NV, typename T, typename R, int VEC>
+template <int NV, typename T, typename R, int VEC, bool ODD>
 cudaError_t run_residual(const ResidualNormArgs &a, const NormPlan &pl, size_t row_bytes, bool bwd, cudaStream_t st) {
     static SmemOptIn opt_in[2];
-    if constexpr (VEC > 1)
+    if constexpr (!ODD)
         if (pl.stages)
-            return bwd ? launch(residual_norm_bwd_kernel<T, R, VEC, NV, true>, a, pl, row_bytes, opt_in[1], st)
-                       : launch(residual_norm_fwd_kernel<T, R, VEC, NV, true>, a, pl, row_bytes, opt_in[0], st);
-    return bwd ? launch(residual_norm_bwd_kernel<T, R, VEC, NV, false>, a, pl, 0, opt_in[1], st)
-               : launch(residual_norm_fwd_kernel<T, R, VEC, NV, false>, a, pl, 0, opt_in[0], st);
+            return bwd ? launch(residual_norm_bwd_kernel<T, R, VEC, NV, kRing>, a, pl, row_bytes, opt_in[1], st)
+                       : launch(residual_norm_fwd_kernel<T, R, VEC, NV, kRing>, a, pl, row_bytes, opt_in[0], st);
+    constexpr int ROWS = ODD ? kOdd : kStraight;
+    return bwd ? launch(residual_norm_bwd_kernel<T, R, VEC, NV, ROWS>, a, pl, 0, opt_in[1], st)
+               : launch(residual_norm_fwd_kernel<T, R, VEC, NV, ROWS>, a, pl, 0, opt_in[0], st);
 }
 
-cudaError_t sum_parts(const float *part, float *o0, float *o1, const NormPlan &pl, int64_t width, cudaStream_t st) {
+cudaError_t sum_parts(const float *part, float *o0, float *o1, const NormPlan &pl, int64_t width, int num_sms, cudaStream_t st) {
     if (!o0 && !o1) return cudaSuccess;
-    const dim3 grid((unsigned)((width + 31) / 32), o1 ? 2u : 1u);
-    norm_sum_kernel<<<grid, 32 * kSumRows, 0, st>>>(part, o0, o1, (int64_t)pl.rblocks * pl.ty, width);
-    return cudaGetLastError();
+    const int64_t parts = (int64_t)pl.rblocks * pl.ty;
+    // 8 columns a block where blocks of 32 would leave SMs idle
+    const int cw = (width + 31) / 32 * (o1 ? 2 : 1) < num_sms ? 8 : 32;
+    // its blocks may take their places while the rows' last blocks run
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((width + cw - 1) / cw), o1 ? 2u : 1u);
+    cfg.blockDim = dim3(kSumThr);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cw == 8 ? norm_sum_kernel<8> : norm_sum_kernel<32>, part, o0, o1, parts, width);
 }
 
-// Vector widths: 8 columns where an array is bf16, 4 where all are fp32, 1 for rows that do not allow 16-byte accesses.
+// Vector widths: 8 columns where an array is bf16, 4 where all are fp32, and 4 column by
+// column for rows that do not allow 16-byte accesses (6190 rows of 398 columns, bf16 and
+// fp32, backward: 21 us, 56 us with one column a thread, whose addresses were most of its work).
 template <typename F>
 cudaError_t with_nv(int nv, F f) {
     switch (nv) {
         case 1: return f(std::integral_constant<int, 1>{});
         case 2: return f(std::integral_constant<int, 2>{});
         case 4: return f(std::integral_constant<int, 4>{});
-        case 8: return f(std::integral_constant<int, 8>{});
-        case 16: return f(std::integral_constant<int, 16>{});
-        default: return f(std::integral_constant<int, 32>{});
+        default: return f(std::integral_constant<int, 8>{});
     }
 }
 
@@ -825,9 +906,10 @@ cudaError_t with_nv(int nv, F f) {
 // Rows of partial sums that a backward of these sizes can need, for any vector width.
 size_t norm_parts(int64_t rows, int64_t width, int64_t groups, int num_sms) {
     size_t most = 0;
-    for (int vec : {8, 4, 1}) {
+    for (int i = 0; i < 3; ++i) {
         const int64_t W = width / groups;
-        const NormPlan pl = plan_norm(rows, W, groups, vec, vectors_for(W, vec), num_sms, true);
+        const int vec = i == 0 ? 8 : 4;
+        const NormPlan pl = plan_norm(rows, W, groups, vec, vectors_for(W, vec, i == 2, true), num_sms, true);
         most = std::max(most, (size_t)pl.rblocks * (size_t)pl.ty);
     }
     return most;
@@ -838,21 +920,20 @@ cudaError_t launch_gated_norm(const GatedNormArgs &a, bool bf16, bool bwd, int n
     const int es = bf16 ? 2 : 4, v = bf16 ? 8 : 4;
     const bool ok = W % v == 0 && vec16(a.x, a.x_sr, es) && vec16(a.z, a.z_sr, es) && vec16(a.y, a.y_sr, es) &&
                     vec16(a.dy, a.y_sr, es) && vec16(a.dx, a.width, es) && vec16(a.dz, a.width, es) && vec16(a.w, 0, 4);
-    const int vec = ok ? v : 1, nv = vectors_for(W, vec);
+    const int vec = ok ? v : 4, nv = vectors_for(W, vec, !ok, bwd);
     NormPlan pl = plan_norm(a.rows, W, a.groups, vec, nv, num_sms, bwd);
     const size_t rb = (size_t)W * es * ((bwd ? 2 : 1) + (a.z ? 1 : 0));
-    add_ring(pl, a.rows, vec, rb, num_sms);
+    add_ring(pl, a.rows, !ok, rb, num_sms);
     cudaError_t e = with_nv(nv, [&](auto n) -> cudaError_t {
         constexpr int NV = decltype(n)::value;
-        if (vec == 1)
-            return bf16 ? run_gated<NV, __nv_bfloat16, 1>(a, pl, rb, bwd, stream) : run_gated<NV, float, 1>(a, pl, rb, bwd, stream);
-        if constexpr (NV <= 8) {
-            if (!bf16) return run_gated<NV, float, 4>(a, pl, rb, bwd, stream);
-            if constexpr (NV <= 4) return run_gated<NV, __nv_bfloat16, 8>(a, pl, rb, bwd, stream);
-        }
+        if (!ok)
+            return bf16 ? run_gated<NV, __nv_bfloat16, 4, true>(a, pl, rb, bwd, stream)
+                        : run_gated<NV, float, 4, true>(a, pl, rb, bwd, stream);
+        if (!bf16) return run_gated<NV, float, 4, false>(a, pl, rb, bwd, stream);
+        if constexpr (NV <= 4) return run_gated<NV, __nv_bfloat16, 8, false>(a, pl, rb, bwd, stream);
         return cudaErrorInvalidConfiguration;
     });
-    if (e == cudaSuccess && bwd) e = sum_parts(a.part, a.dw, nullptr, pl, a.width, stream);
+    if (e == cudaSuccess && bwd) e = sum_parts(a.part, a.dw, nullptr, pl, a.width, num_sms, stream);
     return e;
 }
 
@@ -863,31 +944,29 @@ cudaError_t launch_residual_norm(const ResidualNormArgs &a, bool bf16, bool res_
     const bool ok = W % v == 0 && vec16(a.x, a.x_sr, es) && vec16(a.res, a.res_sr, rs) && vec16(a.y, a.y_sr, es) &&
                     vec16(a.dy, a.y_sr, es) && vec16(a.res_out, a.ro_sr, rs) && vec16(a.dres_out, a.res_sr, rs) &&
                     vec16(a.dx, a.width, es) && vec16(a.dres, a.width, rs) && vec16(a.w, 0, 4) && vec16(a.cs, 0, 4);
-    const int vec = ok ? v : 1, nv = vectors_for(W, vec);
+    const int vec = ok ? v : 4, nv = vectors_for(W, vec, !ok, bwd);
     NormPlan pl = plan_norm(a.rows, W, 1, vec, nv, num_sms, bwd);
     const size_t rb = (size_t)W * (bwd ? rs * (a.dres_out ? 2 : 1) + es * (a.dcs ? 2 : 1) : es + (a.res ? rs : 0));
-    add_ring(pl, a.rows, vec, rb, num_sms);
+    add_ring(pl, a.rows, !ok, rb, num_sms);
     cudaError_t e = with_nv(nv, [&](auto n) -> cudaError_t {
         constexpr int NV = decltype(n)::value;
-        if (vec == 1) {
+        if (!ok) {
             if (bf16)
-                return res_bf16 ? run_residual<NV, __nv_bfloat16, __nv_bfloat16, 1>(a, pl, rb, bwd, stream)
-                                : run_residual<NV, __nv_bfloat16, float, 1>(a, pl, rb, bwd, stream);
-            return res_bf16 ? run_residual<NV, float, __nv_bfloat16, 1>(a, pl, rb, bwd, stream)
-                            : run_residual<NV, float, float, 1>(a, pl, rb, bwd, stream);
+                return res_bf16 ? run_residual<NV, __nv_bfloat16, __nv_bfloat16, 4, true>(a, pl, rb, bwd, stream)
+                                : run_residual<NV, __nv_bfloat16, float, 4, true>(a, pl, rb, bwd, stream);
+            return res_bf16 ? run_residual<NV, float, __nv_bfloat16, 4, true>(a, pl, rb, bwd, stream)
+                            : run_residual<NV, float, float, 4, true>(a, pl, rb, bwd, stream);
         }
-        if constexpr (NV <= 8) {
-            if (vec == 4) return run_residual<NV, float, float, 4>(a, pl, rb, bwd, stream);
-            if constexpr (NV <= 4) {
-                if (bf16)
-                    return res_bf16 ? run_residual<NV, __nv_bfloat16, __nv_bfloat16, 8>(a, pl, rb, bwd, stream)
-                                    : run_residual<NV, __nv_bfloat16, float, 8>(a, pl, rb, bwd, stream);
-                return run_residual<NV, float, __nv_bfloat16, 8>(a, pl, rb, bwd, stream);
-            }
+        if (vec == 4) return run_residual<NV, float, float, 4, false>(a, pl, rb, bwd, stream);
+        if constexpr (NV <= 4) {
+            if (bf16)
+                return res_bf16 ? run_residual<NV, __nv_bfloat16, __nv_bfloat16, 8, false>(a, pl, rb, bwd, stream)
+                                : run_residual<NV, __nv_bfloat16, float, 8, false>(a, pl, rb, bwd, stream);
+            return run_residual<NV, float, __nv_bfloat16, 8, false>(a, pl, rb, bwd, stream);
         }
         return cudaErrorInvalidConfiguration;
     });
-    if (e == cudaSuccess && bwd) e = sum_parts(a.part, a.dw, a.dcs, pl, a.width, stream);
+    if (e == cudaSuccess && bwd) e = sum_parts(a.part, a.dw, a.dcs, pl, a.width, num_sms, stream);
     return e;
 }
 

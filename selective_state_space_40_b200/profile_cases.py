@@ -12,8 +12,12 @@ state update at b256 d5120 N16), bwd130m_b4 (training forward with saved
 states, then the backward, 130M-class layer with 4 batch rows), ssd2p7b_b2
 (Mamba-2 SSD layer, 2.7B-class with 2 batch rows), ssddec_b64 (its one-token
 state update for 64 sequences), ssdcb2p7b (the per-chunk
-C B^T of that layer on the tcgen05 tensor cores, 4 batch rows). Each kernel
-of the case runs REPEATS times (default 3).
+C B^T of that layer on the tcgen05 tensor cores, 4 batch rows), linattn_b8
+(linear attention with a decay per head, 8 x 2048 tokens, 24 heads of 64),
+linattn_bwd (its gradients, 2 x 4001 tokens, 16 heads of 128 and 96 columns in
+groups of 4), linattn_step (one token of 64 sequences, 80 heads of 128 x 64),
+gnorm_bwd (gated norm's gradients, 8192 rows of 5120), rnorm_bwd (residual
+norm's gradients, 8192 rows of 2560). Each kernel of the case runs REPEATS times (default 3).
 """
 from __future__ import annotations
 
@@ -90,6 +94,42 @@ def _ssd_cb(reps):
         mb.ssd_chunk_cb(g["B"], g["C"], cb=cb)
 
 
+def _rand(*shape, dtype=torch.bfloat16):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(sum(shape))).to(dtype).cuda()
+
+
+def _linattn(reps):
+    q, k, v = (_rand(8, 2048, 24, 64) for _ in range(3))
+    g = torch.full((24,), -0.02, device="cuda")
+    for _ in range(reps):
+        mb.linattn_fwd(q, k, v, g)
+
+
+def _linattn_bwd(reps):
+    q, k, v, do = _rand(2, 4001, 16, 128), _rand(2, 4001, 4, 128), _rand(2, 4001, 4, 96), _rand(2, 4001, 16, 96)
+    g, s0 = torch.full((16,), -0.02, device="cuda"), _rand(2, 16, 128, 96, dtype=torch.float32)
+    for _ in range(reps):
+        mb.linattn_bwd(q, k, v, g, do, initial_state=s0, dfinal=s0)
+
+
+def _linattn_step(reps):
+    state, g = _rand(64, 80, 128, 64, dtype=torch.float32), torch.full((80,), -0.02, device="cuda")
+    q, k, v = _rand(64, 80, 128), _rand(64, 80, 128), _rand(64, 80, 64)
+    for _ in range(reps):
+        mb.linattn_state_update(state, q, k, v, g)
+
+
+def _norm_bwd(reps, gated):
+    rows, width = 8192, 5120 if gated else 2560
+    x, z, dy, w = _rand(rows, width), _rand(rows, width), _rand(rows, width), _rand(width, dtype=torch.float32)
+    r = None if gated else _rand(rows, width, dtype=torch.float32)
+    for _ in range(reps):
+        if gated:
+            mb.gated_norm_bwd(x, z, w, dy, gate_first=True)
+        else:
+            mb.residual_norm_bwd(r, w, dy, r, x=x, channel_scale=w)
+
+
 CASES = {
     "scan130m": lambda r: _scan(r),
     "scan130m_reg": lambda r: _scan(r, plan=(4, 1, 0, mb.MS_ENGINE_REGISTER)),
@@ -102,6 +142,11 @@ CASES = {
     "ssd2p7b_b2": _ssd,
     "ssddec_b64": _ssd_decode,
     "ssdcb2p7b": _ssd_cb,
+    "linattn_b8": _linattn,
+    "linattn_bwd": _linattn_bwd,
+    "linattn_step": _linattn_step,
+    "gnorm_bwd": lambda r: _norm_bwd(r, True),
+    "rnorm_bwd": lambda r: _norm_bwd(r, False),
 }
 
 

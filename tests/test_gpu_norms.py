@@ -83,6 +83,14 @@ def test_gated_norm(dtype, first, rows, width, groups):
                 rand(s + 3, rows, width, dtype=dtype), groups, 1e-5, first, dtype)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,width,groups", [(1500, 130, 1), (2100, 33 * 5, 5), (700, 1503, 1), (400, 4001, 1), (333, 7 * 90, 7)])
+def test_gated_norm_many_rows_of_any_width(dtype, rows, width, groups):
+    s = rows + width
+    check_gated(rand(s, rows, width, dtype=dtype), rand(s + 1, rows, width, dtype=dtype, mul=2.0), 1 + 0.3 * rand(s + 2, width),
+                rand(s + 3, rows, width, dtype=dtype), groups, 1e-5, groups == 1, dtype)
+
+
 @pytest.mark.parametrize("width", [8191, 10001, 16383, 16384])
 def test_gated_norm_widest(width):
     check_gated(rand(1, 3, width, dtype=BF), rand(2, 3, width, dtype=BF), None, rand(3, 3, width, dtype=BF), 1, 1e-5, True, BF)
@@ -165,6 +173,12 @@ def test_residual_norm(dtype, rdtype, rows, width):
     x, res = rand(s, rows, width, dtype=dtype), rand(s + 1, rows, width, dtype=rdtype, mul=2.0)
     check_residual(x, res, 1 + 0.2 * rand(s + 2, width), 0.5 + 0.2 * rand(s + 3, width), rand(s + 4, rows, width, dtype=dtype),
                    rand(s + 5, rows, width, dtype=rdtype), 0.7, 1e-5, dtype, rdtype)
+
+
+@pytest.mark.parametrize("dtype,rdtype", [(BF, F32), (F32, F32), (F32, BF)])
+@pytest.mark.parametrize("rows,width", [(2000, 398), (900, 1503), (400, 2562), (1200, 61)])
+def test_residual_norm_many_rows_of_any_width(dtype, rdtype, rows, width):
+    test_residual_norm(dtype, rdtype, rows, width)
 
 
 @pytest.mark.parametrize("dtype,rdtype", [(BF, F32), (F32, F32)])
