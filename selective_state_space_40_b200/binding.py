@@ -694,7 +694,11 @@ def state_update(state, x, delta, A, B, C, D=None, z=None, delta_bias=None, soft
 
 # ------------------------------------------- linear attention and its norms ----
 
-_cuda = None  # torch's own entry points for the current device and stream, looked up once
+# The conveniences below are called for single tokens too, where the host's time is what a call takes: they look
+# up torch's own things once, and each tensor's attributes as few times as they can.
+_cuda = None  # torch's entry points for the current device and stream
+_f32 = _empty_like = None  # torch.float32, torch.empty_like
+_codes = {}   # the library's codes of types
 
 
 # The conveniences below run under ``stream`` where one is given, what they allocate too:
@@ -720,13 +724,26 @@ def _layer_call(ref, *others):
     return _cuda[1](dev)
 
 
+def _look_up():
+    global _f32, _empty_like
+    torch = _torch()
+    _f32, _empty_like = torch.float32, torch.empty_like
+    _codes.update({torch.float32: MS_F32, torch.bfloat16: MS_BF16})
+    return _f32
+
+
+def _code(t) -> int:
+    code = _codes.get(t.dtype)
+    return _dtype_code(t) if code is None else code
+
+
 def _same_type(t, shape, dtype, name):
     if t is not None and (t.shape != shape or t.dtype != dtype or (t.stride(-1) != 1 and t.numel() > 0)):
         raise ValueError(f"{name} must be {tuple(shape)} {dtype} with unit stride along its last dimension")
 
 
 def _dense_f32(t, shape, name):
-    if t is not None and (t.shape != shape or t.dtype != _torch().float32 or not t.is_contiguous()):
+    if t is not None and (t.shape != shape or t.dtype != (_f32 or _look_up()) or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {tuple(shape)}")
 
 
@@ -748,11 +765,11 @@ def linattn_dims_for(q, k, v, o, seq_start=None) -> LinattnDims:
         n = seq_start.shape[0] - 1
         qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
         return LinattnDims(n, 0, total, H, k.shape[1], dk, v.shape[2], 0, qs[0], qs[1], 0, ks[0], ks[1], 0, vs[0],
-                           vs[1], 0, os_[0], os_[1], _dtype_code(q))
+                           vs[1], 0, os_[0], os_[1], _code(q))
     b, L, H, dk = q.shape
     qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
     return LinattnDims(b, L, 0, H, k.shape[2], dk, v.shape[3], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1],
-                       vs[2], os_[0], os_[1], os_[2], _dtype_code(q))
+                       vs[2], os_[0], os_[1], os_[2], _code(q))
 
 
 def _check_linattn(q, k, v, log_decay, seq_start):
@@ -760,16 +777,19 @@ def _check_linattn(q, k, v, log_decay, seq_start):
     want = 4 if seq_start is None else 3
     if q.dim() != want or k.dim() != want or v.dim() != want:
         raise ValueError(f"q, k, v must have {want} dimensions")
-    lead, H, dk, G = q.shape[:-2], q.shape[-2], q.shape[-1], k.shape[-2]
-    _same_type(q, q.shape, q.dtype, "q")
-    _same_type(k, (*lead, G, dk), q.dtype, "k")
-    _same_type(v, (*lead, G, v.shape[-1]), q.dtype, "v")
+    *lead, H, dk = q.shape
+    G, dv, t = k.shape[-2], v.shape[-1], q.dtype
+    if (k.shape != (*lead, G, dk) or v.shape != (*lead, G, dv) or k.dtype != t or v.dtype != t or q.stride(-1) != 1
+            or k.stride(-1) != 1 or v.stride(-1) != 1):
+        _same_type(q, q.shape, t, "q")
+        _same_type(k, (*lead, G, dk), t, "k")
+        _same_type(v, (*lead, G, dv), t, "v")
     _dense_f32(log_decay, (H,), "log_decay")
     if seq_start is None:
-        return q.shape[0], H, dk, v.shape[-1], (*lead, H, v.shape[-1])
+        return lead[0], H, dk, dv, (*lead, H, dv)
     if seq_start.dtype != torch.int32 or seq_start.dim() != 1 or seq_start.shape[0] < 1 or not seq_start.is_contiguous():
         raise ValueError("seq_start must be a contiguous int32 tensor of shape (sequences + 1,)")
-    return seq_start.shape[0] - 1, H, dk, v.shape[-1], (*lead, H, v.shape[-1])
+    return seq_start.shape[0] - 1, H, dk, dv, (*lead, H, dv)
 
 
 def linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, seq_start=None, initial_state=None, o=None,
@@ -788,7 +808,7 @@ def linattn_fwd(q, k, v, log_decay, scale: Optional[float] = None, seq_start=Non
                                return_final_state, None, dev_status, workspace)
     n, H, dk, dv, oshape = _check_linattn(q, k, v, log_decay, seq_start)
     if o is None:
-        o = q.new_empty(oshape)
+        o = _new(q) if dk == dv else q.new_empty(oshape)
     else:
         _same_type(o, oshape, q.dtype, "o")
     fs = final_state
@@ -854,20 +874,22 @@ def linattn_state_update(state, q, k, v, log_decay, scale: Optional[float] = Non
     b, H, dk = q.shape
     G, dv = v.shape[1], v.shape[2]
     ss = state.stride()
-    if state.shape != (b, H, dk, dv) or state.dtype != _torch().float32 or ss[2:] != (dv, 1):
+    if state.shape != (b, H, dk, dv) or state.dtype != (_f32 or _look_up()) or ss[2:] != (dv, 1):
         raise ValueError(f"state must be {(b, H, dk, dv)} fp32 with dense [dk, dv] blocks")
-    _same_type(q, q.shape, q.dtype, "q")
-    _same_type(k, (b, G, dk), q.dtype, "k")
-    _same_type(v, (b, G, dv), q.dtype, "v")
+    qs, ks, vs, t = q.stride(), k.stride(), v.stride(), q.dtype
+    if k.shape != (b, G, dk) or v.shape != (b, G, dv) or k.dtype != t or v.dtype != t or qs[2] != 1 or ks[2] != 1 or vs[2] != 1:
+        _same_type(q, q.shape, t, "q")
+        _same_type(k, (b, G, dk), t, "k")
+        _same_type(v, (b, G, dv), t, "v")
     _dense_f32(log_decay, (H,), "log_decay")
     if o is None:
-        o = q.new_empty((b, H, dv))
+        o = _new(q) if dk == dv else q.new_empty((b, H, dv))
     else:
         _same_type(o, (b, H, dv), q.dtype, "o")
     st = _layer_call(state, q, k, v, log_decay, o, dev_status)
-    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
+    os_ = o.stride()
     dims = LinattnUpdateDims(b, H, G, dk, dv, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], ss[0], ss[1],
-                             _dtype_code(q))
+                             _code(q))
     rc = mamba_linattn_state_update(_ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
                                     dk ** -0.5 if scale is None else scale, _ptr(o), dims, _ptr(dev_status), st)
     if rc != MS_OK:
@@ -881,8 +903,17 @@ def _rows(t, name, shape, dtype):
         return 0
     if len(shape) != 2:
         raise ValueError(f"{name} must be [rows, width]")
-    _same_type(t, shape, dtype, name)
-    return t.stride(0)
+    s = t.stride()
+    if t.shape != shape or t.dtype != dtype or s[1] != 1:
+        _same_type(t, shape, dtype, name)
+    return s[0]
+
+
+def _new(x, dtype=None):
+    """An uninitialised dense tensor of x's shape (of rows: contiguous)."""
+    if _empty_like is None:
+        _look_up()
+    return _empty_like(x, dtype=dtype) if dtype is not None else _empty_like(x)
 
 
 def gated_norm_fwd(x, z=None, weight=None, groups: int = 1, eps: float = 1e-5, gate_first: bool = False, y=None,
@@ -895,11 +926,11 @@ def gated_norm_fwd(x, z=None, weight=None, groups: int = 1, eps: float = 1e-5, g
             return gated_norm_fwd(x, z, weight, groups, eps, gate_first, y, None, dev_status)
     xs = _rows(x, "x", x.shape, x.dtype)
     zs = _rows(z, "z", x.shape, x.dtype)
-    _dense_f32(weight, x.shape[1:], "weight")
+    _dense_f32(weight, (x.shape[1],), "weight")
     if y is None:
-        y = x.new_empty(x.shape)
+        y = _new(x)
     st = _layer_call(x, z, weight, y, dev_status)
-    dims = GatedNormDims(x.shape[0], x.shape[1], groups, xs, zs, _rows(y, "y", x.shape, x.dtype), eps, _dtype_code(x),
+    dims = GatedNormDims(x.shape[0], x.shape[1], groups, xs, zs, _rows(y, "y", x.shape, x.dtype), eps, _code(x),
                          int(gate_first))
     rc = mamba_gated_norm_fwd(_ptr(x), _ptr(z), _ptr(weight), _ptr(y), dims, _ptr(dev_status), st)
     if rc != MS_OK:
@@ -917,13 +948,12 @@ def gated_norm_bwd(x, z, weight, dy, groups: int = 1, eps: float = 1e-5, gate_fi
     torch = _torch()
     xs = _rows(x, "x", x.shape, x.dtype)
     zs = _rows(z, "z", x.shape, x.dtype)
-    _dense_f32(weight, x.shape[1:], "weight")
-    g = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device),
-         "dz": torch.empty(x.shape, dtype=x.dtype, device=x.device) if z is not None else None,
+    _dense_f32(weight, (x.shape[1],), "weight")
+    g = {"dx": _new(x), "dz": _new(x) if z is not None else None,
          "dweight": torch.empty(x.shape[1], dtype=torch.float32, device=x.device) if want_dweight else None}
     st = _layer_call(x, z, weight, dy, dev_status, workspace)
     dims = GatedNormDims(x.shape[0], x.shape[1], groups, xs, zs, _rows(dy, "dy", x.shape, x.dtype), eps,
-                         _dtype_code(x), int(gate_first))
+                         _code(x), int(gate_first))
     ws, wp, wb = _workspace(workspace, mamba_gated_norm_bwd_workspace_size(dims) if want_dweight else 0, x.device)
     rc = mamba_gated_norm_bwd(_ptr(x), _ptr(z), _ptr(weight), _ptr(dy), _ptr(g["dx"]), _ptr(g["dz"]),
                               _ptr(g["dweight"]), dims, wp, wb, _ptr(dev_status), st)
@@ -948,15 +978,15 @@ def residual_norm_fwd(x, residual=None, weight=None, eps: float = 1e-5, res_scal
     rt = residual.dtype if residual is not None else residual_out.dtype if residual_out is not None else \
         residual_dtype or x.dtype
     if residual_out is None:
-        residual_out = x.new_empty(shape, dtype=rt)
+        residual_out = _new(x, rt)
     if y is None:
-        y = x.new_empty(shape)
-    _dense_f32(weight, shape[1:], "weight")
-    _dense_f32(channel_scale, shape[1:], "channel_scale")
+        y = _new(x)
+    _dense_f32(weight, (shape[1],), "weight")
+    _dense_f32(channel_scale, (shape[1],), "channel_scale")
     st = _layer_call(x, residual, weight, channel_scale, y, residual_out, dev_status)
     dims = ResidualNormDims(shape[0], shape[1], xs, _rows(residual, "residual", shape, rt),
                             _rows(y, "y", shape, x.dtype), _rows(residual_out, "residual_out", shape, rt), eps,
-                            res_scale, _dtype_code(x), _dtype_code(residual_out))
+                            res_scale, _code(x), _code(residual_out))
     rc = mamba_residual_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(channel_scale), _ptr(y),
                                  _ptr(residual_out), dims, _ptr(dev_status), st)
     if rc != MS_OK:
@@ -976,19 +1006,18 @@ def residual_norm_bwd(residual_out, weight, dy, dresidual_out=None, x=None, eps:
     torch = _torch()
     shape = dy.shape
     rs = _rows(residual_out, "residual_out", shape, residual_out.dtype)
-    _dense_f32(weight, shape[1:], "weight")
-    _dense_f32(channel_scale, shape[1:], "channel_scale")
+    _dense_f32(weight, (shape[1],), "weight")
+    _dense_f32(channel_scale, (shape[1],), "channel_scale")
     with_c = x is not None and channel_scale is not None
     f32 = dict(dtype=torch.float32, device=dy.device)
-    g = {"dx": torch.empty(shape, dtype=dy.dtype, device=dy.device),
-         "dresidual": torch.empty(shape, dtype=residual_out.dtype, device=dy.device),
+    g = {"dx": _new(dy), "dresidual": _new(dy, residual_out.dtype),
          "dweight": torch.empty(shape[1], **f32) if want_dweight else None,
          "dchannel_scale": torch.empty(shape[1], **f32) if with_c else None}
     st = _layer_call(dy, residual_out, weight, dresidual_out, x, channel_scale, dev_status, workspace)
     dims = ResidualNormDims(shape[0], shape[1], _rows(x, "x", shape, dy.dtype),
                             _rows(dresidual_out, "dresidual_out", shape, residual_out.dtype),
-                            _rows(dy, "dy", shape, dy.dtype), rs, eps, res_scale, _dtype_code(dy),
-                            _dtype_code(residual_out))
+                            _rows(dy, "dy", shape, dy.dtype), rs, eps, res_scale, _code(dy),
+                            _code(residual_out))
     need = mamba_residual_norm_bwd_workspace_size(dims) if want_dweight or with_c else 0
     ws, wp, wb = _workspace(workspace, need, dy.device)
     rc = mamba_residual_norm_bwd(_ptr(residual_out), _ptr(weight), _ptr(dy), _ptr(dresidual_out), _ptr(x),
