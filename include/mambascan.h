@@ -423,7 +423,8 @@ int mamba2_ssd_state_update(float *state, const void *x, const void *dt, const f
  * except where that is said.
  * dk and dv are 1..128, all arrays of one type, bf16 or fp32. bf16 rows that
  * start on 16-byte boundaries (every pointer and stride) with dk and dv
- * multiples of 8 run on the tcgen05 tensor cores in chunks of 128 tokens:
+ * multiples of 8 run on the tcgen05 tensor cores in chunks of 128 tokens
+ * (unless no sequence can have more than 8):
  * the products' operands are bf16, so the scores (and, read by a query, the
  * state) are rounded once to bf16; the running state itself stays fp32 and
  * takes its updates at full precision. There, finite inputs are assumed: a

@@ -499,3 +499,11 @@ def test_conveniences_on_another_stream():
     for m in ("dq", "dk", "dv", "dinitial_state"):
         assert torch.equal(want[m], got[m])
     assert torch.equal(o3, mb.linattn_state_update(fin, q[:1], k[:1], v[:1], g)) and torch.equal(fin, fin2)
+
+
+@pytest.mark.parametrize("L", [3, 7, 8, 9, 12])
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 40)])
+def test_few_tokens(L, dk, dv):
+    """On both sides of the number of tokens from which chunks are used: dense, packed, and shared heads."""
+    run_dense(make(3 * L, 4, 2, dk, dv, BF, 70 + L, n=3), 3, L, BF)
+    run_packed(make(L, 4, 2, dk, dv, BF, 80 + L, n=4), [0, 1, 1, 3, L], BF)
