@@ -82,6 +82,11 @@ constexpr uint32_t kFlagTries = 1u << 22;   // polls of a predecessor's flag
 __host__ __device__ constexpr uint32_t col_qk(int b) { return 128u * b; }
 __host__ __device__ constexpr uint32_t col_oa(int b) { return 128u * b + 64u; }
 constexpr uint32_t kColOb = 256, kColKv = 320;
+// The first pass of kStates has no QK and O. So KV has two buffers, in the columns and with the barriers of QK and
+// P, the warps of P form half of Z', those of E keep half of the state at dx = 128, and there are three stages
+// (65536 tokens, 16 heads of 128: 190 -> 183, 150, 138 us of that pass with two buffers, P's and E's warps; two buffers
+// of Z' at the cost of a stage: 178).
+__host__ __device__ constexpr uint32_t col_kv(bool own, int cc) { return own ? 256u * (cc & 1) : kColKv; }
 
 struct TcProblem {
     int mx, my, mz;  // tensor maps of x, y, z
@@ -130,12 +135,13 @@ struct Smem {
     static constexpr int kY = kC * DX * 2;
     static constexpr int kZb = kC * kZ * 2;
     static constexpr int kStage = kX + kY + kZb;
-    static constexpr int kStages = DX == 64 ? 3 : 2;
+    static constexpr int kStages = DX == 64 || kOwn ? 3 : 2;
     static constexpr int oZs = kStages * kStage;               // three parts of Z'
     static constexpr int oS = oZs + 3 * kZb;                   // S in bf16
     // states on their way, a part per warp of group S: at dx = 128 the warp's own rows of the S tile
     static constexpr int oMove = DX == 64 ? oS + DX * kZ * 2 : oS;
-    static constexpr int oItem = oMove + DX * kZ * 2;          // two items
+    static constexpr bool kS2 = kOwn && DX == 128;             // eight warps keep the state: group S, and E's
+    static constexpr int oItem = oMove + (kS2 ? 2 : 1) * DX * kZ * 2;  // two items
     // two items' tables: lam^n, n = 0..128; lam^|d| at 31 + d, d = t - s, 0 on the masked side;
     // lam^(31-c), in reverse lam^c, c < 32
     static constexpr int oTab = oItem + 2 * (int)sizeof(Item);
@@ -462,11 +468,12 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
             int n = 1;
             if (i >= kBarXFree && i < kBarYFree) n = 2;
             else if (i >= kBarYFree && i < kBarZFree) n = kOwn ? 1 : 2;
-            else if (i >= kBarZFree && i < kBarQK) n = 4;  // the warps of E, of V where there is no E
-            else if ((i >= kBarP && i < kBarO) || (i >= kBarOFree && i < kBarZs) || i == kBarKVFree || i == kBarS) n = 4;
+            else if (i >= kBarZFree && i < kBarQK) n = kOwn ? 8 : 4;  // the warps of E, of V where there is no E
+            else if (i >= kBarP && i < kBarO) n = M::kS2 ? 8 : 4;
+            else if ((i >= kBarOFree && i < kBarZs) || i == kBarKVFree || i == kBarS) n = 4;
             else if ((i >= kBarZs && i < kBarZsFree) || (i >= kBarClear && i < kBarItem)) n = 4;
             else if (i >= kBarZRead && i < kBarEnd) n = 4;
-            else if (i >= kBarItemFree && i < kBarZRead) n = kOwn ? 9 : 19;  // every role's warps
+            else if (i >= kBarItemFree && i < kBarZRead) n = M::kS2 ? 17 : kOwn ? 13 : 19;  // every role's warps
             bar_init(bars + 8 * i, n);
         }
         misc[1] = 0u;
@@ -628,7 +635,8 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
 #pragma unroll 1
             for (int c = 0; c < nc; ++c, ++cc, ring.next()) {
                 const int st = ring.st;
-                if (!wait_all(kBarY + st, ring.use) || (cc > 0 && !wait_all(kBarKVFree, cc - 1))) return false;
+                if (!wait_all(kBarY + st, ring.use)) return false;
+                if (kOwn ? cc >= 2 && !wait_all(kBarP + (cc & 1), (cc - 2) >> 1) : cc > 0 && !wait_all(kBarKVFree, cc - 1)) return false;
 #pragma unroll 1
                 for (int hf = 0; hf < 2; ++hf) {
                     if (!wait_all(kBarZs + hf, cc)) return false;
@@ -637,10 +645,10 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
                         const uint64_t y = dstep(dy0, st * M::kStage + 8192 * hf), z = dstep(dz, 8192 * hf);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma(tmem + kColKv, dstep(y, 2048 * k), dstep(z, 2048 * k), idesc(3 * kZ, true, true), hf > 0 || k > 0);
+                            mma(tmem + col_kv(kOwn, cc), dstep(y, 2048 * k), dstep(z, 2048 * k), idesc(3 * kZ, true, true), hf > 0 || k > 0);
                         mma_commit(bar(kBarZsFree + hf));
                         if (hf == 1) {
-                            mma_commit(bar(kBarKV));
+                            mma_commit(bar(kOwn ? kBarQK + (cc & 1) : kBarKV));
                             mma_commit(bar(kBarYFree + st));
                         }
                     }
@@ -687,7 +695,7 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
             });
             drain(2);
         }
-    } else if (warp < 4) {
+    } else if (!kOwn && warp < 4) {
         // ================================= group P =================================
         if constexpr (!kOwn) {
             const int t = 32 * warp + lane;
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
                 return true;
             });
         }
-    } else if (warp >= R::kE0) {
+    } else if (!M::kS2 && warp >= R::kE0) {
         // ================================= group E =================================
         if constexpr (!kOwn) {
             const int t0 = 32 * (warp - R::kE0), t = t0 + lane;
@@ -834,7 +842,8 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
     } else if (warp < R::kS0) {
         // ================================= group V =================================
         constexpr int VT = 128, kItems = kC * 8 / VT / 2;  // 16-byte pieces a thread has in each half
-        const int gt = tid - 32 * R::kV0;
+        // (the first pass of kStates has no P: its warps are a second group V, each has half of the tokens)
+        const int gt = tid & (VT - 1), hf0 = kOwn && warp < R::kV0 ? 1 : 0, hf1 = kOwn ? hf0 + 1 : 2;
         const uint32_t zs = sbase + M::oZs + 16u * gt;
         each_item([&](const Item &it, const float *tab) {
             const TcProblem &p = a.p[it.pi];
@@ -850,19 +859,19 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
                     // the rows behind the sequence, before any product reads them
                     if (!wait_all(kBarY + st, ring.use)) return false;
 #pragma unroll 1
-                    for (int i = n * 8 + gt; i < kC * 8; i += VT) {
+                    for (int i = (n > 64 * hf0 ? n : 64 * hf0) * 8 + gt; i < 64 * 8 * hf1; i += VT) {
                         sts128(y + M::kY + 16 * i, 0, 0, 0, 0);
 #pragma unroll
                         for (int j = 0; j < DX / 64; ++j) sts128(y + j * 16384 + 16 * i, 0, 0, 0, 0);
                     }
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(bar(kBarClear + st));
+                    if (!kOwn && lane == 0) bar_arrive(bar(kBarClear + st));
                 }
                 // the weight of row gt / 8 + VT / 8 k
                 const float *pw = tab + M::kPw + (rev ? (gt >> 3) + 1 : n - 1 - (gt >> 3));
 #pragma unroll 1
-                for (int hf = 0; hf < 2; ++hf) {
+                for (int hf = hf0; hf < hf1; ++hf) {
                     if (cc > 0 && !wait_all(kBarZsFree + hf, cc - 1)) return false;
 #pragma unroll 1
                     for (int k = kItems * hf; k < kItems * (hf + 1); ++k) {
@@ -885,7 +894,8 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
                     __syncwarp();
                     if (lane == 0) {
                         bar_arrive(bar(kBarZs + hf));
-                        if (hf == 1) bar_arrive(bar((kOwn ? kBarZFree : kBarZRead) + st));
+                        if (kOwn) bar_arrive(bar(kBarZFree + st));
+                        else if (hf == 1) bar_arrive(bar(kBarZRead + st));
                     }
                 }
             }
@@ -894,10 +904,11 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
     } else {
         // ================================= group S =================================
         // dx <= 64: KV's second 64 rows repeat the first, so warps 2 and 3 take the
-        // second 32 columns of rows 0..63
-        constexpr int NCOL = DX == 64 ? 32 : 64;
-        const int w = warp - R::kS0, row = (DX == 64 ? 32 * (w & 1) : 32 * w) + lane, c0 = DX == 64 ? 32 * (w >> 1) : 0;
-        const uint32_t kv = tmem + ((uint32_t)(32 * w) << 16) + kColKv + (uint32_t)c0;
+        // second 32 columns of rows 0..63. In the first pass of kStates at dx = 128 group E's warps take the second 32
+        constexpr int NCOL = DX == 64 || M::kS2 ? 32 : 64;
+        const int w = warp - R::kS0, row = (DX == 64 ? 32 * (w & 1) : 32 * (w & 3)) + lane;
+        const int c0 = DX == 64 ? 32 * (w >> 1) : M::kS2 ? 32 * (w >> 2) : 0;
+        const uint32_t kv0 = tmem + ((uint32_t)(32 * (w & 3)) << 16) + (uint32_t)c0;
         const uint32_t dst = sbase + M::oS + 128u * row;
         const int x8 = row & 7, j0 = c0 >> 3;
         // A thread holds a row (or half of one); states come and go through a part of shared memory
@@ -1025,8 +1036,9 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
                 const f2 k2 = f2_splat(c == cpart ? keepp : keep), p2 = f2_splat(c == cpart ? partp : part);
 #pragma unroll
                 for (int i = 0; i < NCOL / 2; ++i) S[i] = f2_fma(p2, S[i], f2_mul(k2, S[i]));
-                if (!wait_all(kBarKV, cc)) return false;
+                if (!(kOwn ? wait_all(kBarQK + (cc & 1), cc >> 1) : wait_all(kBarKV, cc))) return false;
                 tc_after();
+                const uint32_t kv = kv0 + col_kv(kOwn, cc);
 #pragma unroll
                 for (int i = 0; i < NCOL; i += 8) {
                     float hi[8], mid[8], lo[8];
@@ -1038,7 +1050,7 @@ __global__ void __launch_bounds__(R::kThreads, 1) linattn_tc_kernel(const __grid
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(bar(kBarKVFree));
+                if (lane == 0) bar_arrive(bar(kOwn ? kBarP + (cc & 1) : kBarKVFree));
             }
             if (kMode == kChained && !kOwn && !it.last) {
                 float4 *to = reinterpret_cast<float4 *>(a.chain) + ((int64_t)chain * (kZ / 4) + c0 / 4) * DX + row;
@@ -1152,7 +1164,7 @@ Plan plan_of(int64_t batch, int64_t rows, bool packed, int64_t H, int units, int
         double best = (double)most;
         for (int r = 1; r <= 3; ++r) {
             const int64_t n = r * num_sms / chains, len = std::max<int64_t>(4, (most + n - 1) / n);
-            const double t = r * (double)(len + 1) * 1.6;  // the first pass takes 0.6 of the main one
+            const double t = r * (double)(len + 1) * 1.45;  // the first pass takes 0.45 of the main one
             if (len < most && t < best) best = t, chunks = len, p.mode = kStates;
         }
     } else if (chains > num_sms && mean >= 4) {
